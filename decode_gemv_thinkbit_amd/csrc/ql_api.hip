@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "ql_internal.hpp"
+#include "ql_mx4.hpp"
 
 namespace {
 
@@ -465,6 +466,116 @@ ql_status qlinear_gemm_grouped(const ql_gemv_desc* descs, int32_t count, int64_t
   return hip_status(ql::launch_gemm_grouped(descs, count, total_tasks, (int)M, static_cast<float*>(workspace),
                                             (int64_t)(workspace_bytes / sizeof(float)), stream),
                     "grouped gemm launch");
+}
+
+// ---------------------------------------------------------------- microscaled 4-bit floats
+static ql_status check_mx4(int64_t N, int64_t K) {
+  if (N <= 0 || K <= 0) return fail(QL_EINVAL, "N and K must be positive (N=%lld, K=%lld)", (long long)N, (long long)K);
+  if (K % 32) return fail(QL_EINVAL, "K=%lld is not a multiple of 32", (long long)K);
+  if (K > ((int64_t)1 << 26) || N > ((int64_t)1 << 36) / K)
+    return fail(QL_EINVAL, "shape too large (N=%lld, K=%lld)", (long long)N, (long long)K);
+  return QL_OK;
+}
+
+static ql_status check_mx4_product(int64_t N, int64_t K) {
+  QL_TRY(check_mx4(N, K));
+  if (N >= ((int64_t)1 << 26)) return fail(QL_EINVAL, "N=%lld must be below 2^26", (long long)N);
+  return QL_OK;
+}
+
+static ql_status check_dtype(int dtype) {
+  if (dtype != QL_F32 && dtype != QL_BF16 && dtype != QL_F16) return fail(QL_EINVAL, "unknown element type %d", dtype);
+  return QL_OK;
+}
+
+int64_t qlinear_mx4_scale_stride(int64_t K) { return check_mx4(1, K) == QL_OK ? ql::mx4_scale_stride(K) : 0; }
+
+ql_status qlinear_mx4_quantize(int64_t N, int64_t K, int dtype, const void* W, uint8_t* codes, uint8_t* scales,
+                               hipStream_t stream) {
+  QL_TRY(check_mx4(N, K));
+  QL_TRY(check_dtype(dtype));
+  QL_TRY(check_ptrs({W, codes, scales}));
+  return hip_status(ql::launch_mx4_quantize(N, K, dtype, W, codes, scales, stream), "mx4_quantize launch");
+}
+
+ql_status qlinear_mx4_dequant(int64_t N, int64_t K, const uint8_t* codes, const uint8_t* scales, int out_bf16,
+                              void* out, hipStream_t stream) {
+  QL_TRY(check_mx4(N, K));
+  QL_TRY(check_ptrs({codes, scales, out}));
+  return hip_status(ql::launch_mx4_dequant(N, K, codes, scales, out_bf16 != 0, out, stream), "mx4_dequant launch");
+}
+
+ql_status qlinear_mx4_gemv(int64_t M, int64_t N, int64_t K, const uint8_t* codes, const uint8_t* scales,
+                           const uint16_t* x, float* y, hipStream_t stream) {
+  if (M < 1 || M > 16) return fail(QL_EINVAL, "mx4_gemv needs 1 <= M <= 16 (M=%lld)", (long long)M);
+  QL_TRY(check_mx4_product(N, K));
+  QL_TRY(check_ptrs({codes, scales, x, y}));
+  return hip_status(ql::launch_mx4_gemv((int)M, (int)N, (int)K, codes, scales, x, y, stream), "mx4_gemv launch");
+}
+
+size_t qlinear_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || M >= ((int64_t)1 << 24) || check_mx4_product(N, K) != QL_OK) return 0;
+  return 0;
+}
+
+ql_status qlinear_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
+                           const uint8_t* codes, const uint8_t* scales, float* y, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  if (M < 1 || M >= ((int64_t)1 << 24)) return fail(QL_EINVAL, "mx4_gemm needs 1 <= M < 2^24 (M=%lld)", (long long)M);
+  QL_TRY(check_mx4(M, K));
+  QL_TRY(check_mx4_product(N, K));
+  QL_TRY(check_ptrs({x_codes, x_scales, codes, scales, y}));
+  const size_t need = qlinear_mx4_gemm_workspace_bytes(M, N, K);
+  if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
+  if (need) QL_TRY(check_ptrs({workspace}));
+  return hip_status(ql::launch_mx4_gemm((int)M, (int)N, (int)K, x_codes, x_scales, codes, scales, y, stream),
+                    "mx4_gemm launch");
+}
+
+// ---------------------------------------------------------------- mixture of experts
+static ql_status check_topk(int64_t T, int64_t E, int64_t k) {
+  if (E < 1 || E > QL_MOE_MAX_EXPERTS)
+    return fail(QL_EINVAL, "1 <= E <= %d experts (E=%lld)", QL_MOE_MAX_EXPERTS, (long long)E);
+  if (k < 1 || k > E || k > QL_MOE_MAX_TOPK)
+    return fail(QL_EINVAL, "1 <= k <= min(E, %d) (k=%lld, E=%lld)", QL_MOE_MAX_TOPK, (long long)k, (long long)E);
+  if (T < 1 || T >= ((int64_t)1 << 30)) return fail(QL_EINVAL, "bad token count %lld", (long long)T);
+  return QL_OK;
+}
+
+ql_status qlinear_moe_route(int64_t T, int64_t E, int64_t k, int renormalize, int dtype, const void* logits,
+                            int32_t* ids, float* weights, hipStream_t stream) {
+  QL_TRY(check_topk(T, E, k));
+  QL_TRY(check_dtype(dtype));
+  QL_TRY(check_ptrs({logits, ids, weights}));
+  return hip_status(ql::launch_moe_route(T, (int)E, (int)k, renormalize != 0, dtype, logits, ids, weights, stream),
+                    "moe_route launch");
+}
+
+static ql_status check_moe_sizes(int64_t T, int64_t k, int64_t H, int64_t I) {
+  if (T < 1 || T > QL_MOE_MAX_TOKENS)
+    return fail(QL_EINVAL, "mx4_moe takes 1..%d tokens (T=%lld)", QL_MOE_MAX_TOKENS, (long long)T);
+  if (k < 1 || k > QL_MOE_MAX_TOPK) return fail(QL_EINVAL, "1 <= k <= %d (k=%lld)", QL_MOE_MAX_TOPK, (long long)k);
+  if (H <= 0 || I <= 0 || H % 32 || I % 32 || H > ((int64_t)1 << 20) || I > ((int64_t)1 << 20))
+    return fail(QL_EINVAL, "H=%lld and I=%lld must be multiples of 32, at most 2^20", (long long)H, (long long)I);
+  return QL_OK;
+}
+
+size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I) {
+  return check_moe_sizes(T, k, H, I) == QL_OK ? ql::mx4_moe_workspace_bytes(T, k, I) : 0;
+}
+
+ql_status qlinear_mx4_moe(const ql_mx4_experts* e, int64_t T, const uint16_t* x, float* y, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  if (!e) return fail(QL_EINVAL, "null experts");
+  QL_TRY(check_moe_sizes(T, e->k, e->H, e->I));
+  QL_TRY(check_topk(T, e->E, e->k));
+  QL_TRY(check_ptrs({e->ids, e->weights, e->gate_codes, e->gate_scales, e->up_codes, e->up_scales, e->down_codes,
+                     e->down_scales, x, y, workspace}));
+  const size_t need = ql::mx4_moe_workspace_bytes(T, e->k, e->I);
+  if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
+  const ql::MoeArgs a{(int32_t)T, e->k, e->E, e->H, e->I, x, e->ids, e->weights, e->gate_codes, e->gate_scales,
+                      e->up_codes, e->up_scales, e->down_codes, e->down_scales, y, workspace};
+  return hip_status(ql::launch_mx4_moe(a, stream), "mx4_moe launch");
 }
 
 ql_status qlinear_read_probe(const void* buf, int64_t bytes, uint32_t* out, hipStream_t stream) {

@@ -55,6 +55,14 @@ class ql_littlebit(ctypes.Structure):
                 ("g", ctypes.c_void_p), ("l", ctypes.c_void_p), ("h", ctypes.c_void_p)]
 
 
+class ql_mx4_experts(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("gate_codes", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
+                ("up_codes", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+                ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
+
+
 def lib():
     """Load libqlinear.so; raise if it has not been built."""
     global _lib
@@ -119,6 +127,21 @@ def lib():
         L.qlinear_c4_to_packed.argtypes = [i64, i64, i32, vp, vp, vp, vp, vp]
         L.qlinear_c4_gemv.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
         L.qlinear_c4_gemv_grouped.argtypes = [vp, ctypes.c_int32, i64, ctypes.c_int32, vp, vp]
+        L.qlinear_mx4_scale_stride.argtypes = [i64]
+        L.qlinear_mx4_scale_stride.restype = i64
+        L.qlinear_mx4_quantize.argtypes = [i64, i64, i32, vp, vp, vp, vp]
+        L.qlinear_mx4_dequant.argtypes = [i64, i64, vp, vp, i32, vp, vp]
+        L.qlinear_mx4_gemv.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
+        L.qlinear_mx4_gemm_workspace_bytes.argtypes = [i64, i64, i64]
+        L.qlinear_mx4_gemm_workspace_bytes.restype = sz
+        L.qlinear_mx4_gemm.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.qlinear_moe_route.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, vp]
+        L.qlinear_mx4_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.qlinear_mx4_moe_workspace_bytes.restype = sz
+        L.qlinear_mx4_moe.argtypes = [vp, i64, vp, vp, vp, sz, vp]
+        for name in ("qlinear_mx4_quantize", "qlinear_mx4_dequant", "qlinear_mx4_gemv", "qlinear_mx4_gemm",
+                     "qlinear_moe_route", "qlinear_mx4_moe"):
+            getattr(L, name).restype = i32
         for name in ("qlinear_block_offsets", "qlinear_quantize", "qlinear_pack", "qlinear_pack_scales",
                      "qlinear_unpack", "qlinear_unpack_scales", "qlinear_dequant", "qlinear_gemv",
                      "qlinear_gemv_grouped", "qlinear_gemv_grouped_noalloc", "qlinear_gemm", "qlinear_gemm_grouped", "qlinear_c4_pack", "qlinear_c4_unpack",
@@ -514,6 +537,200 @@ def gemm(x: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     _check(lib().qlinear_gemm(M, pw.N, pw.K, pw.grid, _ptr(pw.blk_grid), _ptr(pw.blk_off), _ptr(pw.packed),
                               _ptr(pw.pscales), _ptr(x), _ptr(out), _ptr(workspace), need, _stream()), "gemm")
+    return out
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floats (MX4)
+MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS = 1024, 16, 64  # QL_MOE_MAX_*
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # ql_dtype
+
+
+@dataclass
+class Mx4Tensor:
+    """A matrix [N, K], or a stack of matrices [count, N, K], of microscaled 4-bit floats: e2m1 codes,
+    two per byte with the even input in the low nibble, and one scale byte s (2^(s - 127)) per 32
+    inputs, each row of scales padded to 4 * ceil(K / 128) bytes."""
+    codes: torch.Tensor       # uint8 [..., N, K/2]
+    scales: torch.Tensor      # uint8 [..., N, 4 * ceil(K/128)]
+
+    def __post_init__(self):
+        c, s = self.codes, self.scales
+        if c.dtype != torch.uint8 or s.dtype != torch.uint8:
+            raise ValueError(f"codes and scales must be torch.uint8, got {c.dtype} and {s.dtype}")
+        if not (c.is_contiguous() and s.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        cs, ss = c.shape, s.shape
+        if len(cs) not in (2, 3) or cs[-1] % 16 or 0 in cs:
+            raise ValueError(f"codes must be [N, K/2] or [count, N, K/2] with K a multiple of 32, got {tuple(cs)}")
+        if ss != cs[:-1] + (4 * ((cs[-1] + 63) // 64),):
+            raise ValueError(f"scales of codes {tuple(cs)} must be [..., N, 4 * ceil(K/128)], got {tuple(ss)}")
+        if c.device != s.device:
+            raise ValueError("codes and scales must be on one device")
+
+    @property
+    def N(self) -> int:
+        return self.codes.shape[-2]
+
+    @property
+    def K(self) -> int:
+        return 2 * self.codes.shape[-1]
+
+    @property
+    def shape(self) -> tuple:
+        return (*self.codes.shape[:-1], self.K)
+
+    @property
+    def nbytes(self) -> int:
+        """Stored bytes of codes and scales (padding included)."""
+        return self.codes.numel() + self.scales.numel()
+
+
+def _launch(what: str, fn, device: torch.device, *args):
+    """Call fn(*args, stream) with the current stream of `device`, made current for the call."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+
+
+def _mx4(t: Mx4Tensor, dims: int, device: torch.device, name: str):
+    if not isinstance(t, Mx4Tensor):
+        raise ValueError(f"{name} must be an Mx4Tensor")
+    if t.codes.dim() != dims:
+        raise ValueError(f"{name} must be {'a matrix' if dims == 2 else 'a stack of matrices'}, got {t.shape}")
+    if t.codes.device != device or not t.codes.is_cuda:
+        raise ValueError(f"{name} must be on the device of the other operands, a CUDA (HIP) device")
+    return t
+
+
+def _result(out: Optional[torch.Tensor], shape: tuple, dtype, device: torch.device, name: str = "out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dev(out, dtype, name)
+    if out.shape != shape or out.device != device:
+        raise ValueError(f"{name} must be {list(shape)} on {device}")
+    return out
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, device: torch.device):
+    if workspace is None or workspace.numel() < need:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _dev(workspace, torch.uint8, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return workspace
+
+
+def mx4_quantize(W: torch.Tensor, out: Optional[Mx4Tensor] = None) -> Mx4Tensor:
+    """W (fp32, bf16 or fp16; [N, K] or [count, N, K], K % 32 == 0) in MX4: per 32 inputs of a row the
+    scale exponent floor(log2 max|w|) - 2 and the nearest codes, ties to even, saturating at 6; blocks
+    with an infinity or NaN read back as NaN."""
+    if W.dtype not in _DTYPES:
+        raise ValueError(f"W must be float32, bfloat16 or float16, got {W.dtype}")
+    _dev(W, W.dtype, "W")
+    if W.dim() not in (2, 3) or W.shape[-1] % 32 or 0 in W.shape:
+        raise ValueError(f"W must be [N, K] or [count, N, K] with K a multiple of 32, got {tuple(W.shape)}")
+    *rows, K = W.shape
+    if out is None:
+        out = Mx4Tensor(torch.empty((*rows, K // 2), dtype=torch.uint8, device=W.device),
+                        torch.empty((*rows, 4 * ((K + 127) // 128)), dtype=torch.uint8, device=W.device))
+    elif _mx4(out, W.dim(), W.device, "out").shape != tuple(W.shape):
+        raise ValueError(f"out must be {tuple(W.shape)}")
+    _launch("mx4_quantize", lib().qlinear_mx4_quantize, W.device, W.numel() // K, K, _DTYPES[W.dtype], W.data_ptr(),
+            out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+def mx4_dequant(t: Mx4Tensor, out_bf16: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of an MX4 tensor, fp32 or bf16 (exact in both)."""
+    _mx4(t, t.codes.dim(), t.codes.device, "t")
+    out = _result(out, t.shape, torch.bfloat16 if out_bf16 else torch.float32, t.codes.device)
+    _launch("mx4_dequant", lib().qlinear_mx4_dequant, out.device, out.numel() // t.K, t.K, t.codes.data_ptr(),
+            t.scales.data_ptr(), 1 if out_bf16 else 0, out.data_ptr())
+    return out
+
+
+def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] fp32 = x [M, K] bf16 times the MX4 weight transposed, M <= 16."""
+    _dev(x, torch.bfloat16, "x")
+    if x.dim() == 1:
+        x = x.view(1, -1)
+    _mx4(w, 2, x.device, "w")
+    M, K = x.shape
+    if K != w.K:
+        raise ValueError(f"x has K={K}, weight has K={w.K}")
+    out = _result(out, (M, w.N), torch.float32, x.device)
+    _launch("mx4_gemv", lib().qlinear_mx4_gemv, x.device, M, w.N, K, w.codes.data_ptr(), w.scales.data_ptr(),
+            x.data_ptr(), out.data_ptr())
+    return out
+
+
+def mx4_gemm(x: Mx4Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] fp32 = x [M, K] times w [N, K] transposed, both MX4 (the scaled matrix instructions)."""
+    _mx4(x, 2, x.codes.device, "x")
+    _mx4(w, 2, x.codes.device, "w")
+    if x.K != w.K:
+        raise ValueError(f"x has K={x.K}, weight has K={w.K}")
+    M, N, K = x.N, w.N, w.K
+    out = _result(out, (M, N), torch.float32, x.codes.device)
+    need = lib().qlinear_mx4_gemm_workspace_bytes(M, N, K)
+    workspace = _scratch(workspace, need, out.device) if need else None
+    _launch("mx4_gemm", lib().qlinear_mx4_gemm, out.device, M, N, K, x.codes.data_ptr(), x.scales.data_ptr(),
+            w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)
+    return out
+
+
+# ---------------------------------------------------------------- mixture of experts
+def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, ids: Optional[torch.Tensor] = None,
+              weights: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The k experts of each token: (ids int32 [T, k], weights fp32 [T, k]) of logits [T, E] (fp32, bf16 or
+    fp16), the largest first and equal ones by ascending expert; weights are the softmax over the chosen
+    experts (renormalize) or over all.  -inf and NaN are never chosen: id -1, weight 0."""
+    if logits.dtype not in _DTYPES:
+        raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _dev(logits, logits.dtype, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if not 1 <= k <= min(E, MOE_MAX_TOPK):
+        raise ValueError(f"k must be 1..{min(E, MOE_MAX_TOPK)}, got {k}")
+    ids = _result(ids, (T, k), torch.int32, logits.device, "ids")
+    weights = _result(weights, (T, k), torch.float32, logits.device, "weights")
+    _launch("moe_route", lib().qlinear_moe_route, logits.device, T, E, k, 1 if renormalize else 0,
+            _DTYPES[logits.dtype], logits.data_ptr(), ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4Tensor, up: Mx4Tensor,
+            down: Mx4Tensor, out: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [T, H] fp32, y[t] = sum_j weights[t, j] * down_e(silu(gate_e x_t) * up_e x_t) with e = ids[t, j], for
+    T <= MOE_MAX_TOKENS tokens: x [T, H] bf16, ids int32 and weights fp32 [T, k] (moe_route's, or another
+    router's; ids outside 0..E-1 are left out), gate and up stacks [E, I, H], down [E, H, I]."""
+    _dev(x, torch.bfloat16, "x")
+    _dev(ids, torch.int32, "ids")
+    _dev(weights, torch.float32, "weights")
+    if x.dim() != 2 or ids.dim() != 2:
+        raise ValueError("x must be [T, H], ids and weights [T, k]")
+    T, H = x.shape
+    k = ids.shape[1]
+    for t, name in ((gate, "gate"), (up, "up"), (down, "down")):
+        _mx4(t, 3, x.device, name)
+    E, I, _ = gate.shape
+    if gate.K != H or up.shape != gate.shape or down.shape != (E, H, I):
+        raise ValueError(f"x [T, {H}] needs gate and up [E, I, {H}] and down [E, {H}, I], got {gate.shape}, "
+                         f"{up.shape}, {down.shape}")
+    if ids.shape != (T, k) or weights.shape != (T, k) or ids.device != x.device or weights.device != x.device:
+        raise ValueError(f"ids and weights must be [{T}, k] on {x.device}")
+    out = _result(out, (T, H), torch.float32, x.device)
+    need = lib().qlinear_mx4_moe_workspace_bytes(T, k, H, I)
+    workspace = _scratch(workspace, max(need, 16), x.device)
+    e = ql_mx4_experts(E, H, I, k, ids.data_ptr(), weights.data_ptr(), gate.codes.data_ptr(), gate.scales.data_ptr(),
+                       up.codes.data_ptr(), up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr())
+    _launch("mx4_moe", lib().qlinear_mx4_moe, x.device, ctypes.byref(e), T, x.data_ptr(), out.data_ptr(),
+            workspace.data_ptr(), need)
     return out
 
 

@@ -388,6 +388,95 @@ size_t qlinear_lb_workspace_bytes(int64_t d_out, int64_t d_in, int64_t rank);
 ql_status qlinear_lb_gemv(const ql_littlebit *w, const uint16_t *x, float *y, void *workspace,
                           size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------- microscaled 4-bit floats (MX4)
+ *
+ * Weights and activations as 4-bit floats with one power-of-two scale per 32 inputs, the
+ * microscaling format whose products gfx950's matrix unit computes directly:
+ *   value = e2m1(code) * 2^(s - 127), code = sign (bit 3) and 0, 0.5, 1, 1.5, 2, 3, 4, 6 for
+ *   bits 0..2 = 0..7; s = 255 makes the block's values NaN.
+ * Storage is row-major, the order such checkpoints use, so no packing step is needed:
+ *   codes  uint8 [N][K/2], the even input in the low nibble; K % 32 == 0;
+ *   scales uint8 [N][qlinear_mx4_scale_stride(K)]: byte b of a row is the scale of inputs
+ *          32b .. 32b+31; rows are padded to whole dwords, and what the padding holds is ignored.
+ * A stack of matrices (experts) is a matrix with count*N rows.  N*K is at most 2^36 elements,
+ * N below 2^26 (the products), K at most 2^26. */
+
+/* Element types of inputs that may come in several. */
+typedef enum { QL_F32 = 0, QL_BF16 = 1, QL_F16 = 2 } ql_dtype;
+
+/* Bytes of one row of scales, 4 * ceil(K / 128); 0 if K is invalid. */
+int64_t qlinear_mx4_scale_stride(int64_t K);
+
+/* Quantize W [N][K] of type dtype: per row and block of 32, s = clamp(floor(log2 max|w|) - 2,
+ * -127, 127) + 127 and each code the nearest e2m1 value to w / 2^(s-127), ties to the even code,
+ * magnitudes above 6 to 6 (a block of zeros: s = 0).  A block holding an infinity or NaN gets
+ * s = 255 and codes 0.  The scale rows' padding is written as 0.
+ *   W (dev) [N][K]; codes (dev) [N][K/2]; scales (dev) [N][scale stride]. */
+ql_status qlinear_mx4_quantize(int64_t N, int64_t K, int dtype, const void *W, uint8_t *codes, uint8_t *scales,
+                               hipStream_t stream);
+
+/* The values as fp32 (out_bf16 == 0) or bf16 bits (exact in both, except that 4 * 2^127 and above,
+ * s = 254, are infinite).  out (dev) [N][K]. */
+ql_status qlinear_mx4_dequant(int64_t N, int64_t K, const uint8_t *codes, const uint8_t *scales, int out_bf16,
+                              void *out, hipStream_t stream);
+
+/* Decode GEMV, 1 <= M <= 16: y[m][n] = sum_k W[n][k] * x[m][k] with W in MX4 and x in bf16.  The
+ * products are exact (bf16 operands on the matrix unit), sums fp32 in a fixed order: deterministic.
+ *   x (dev) bf16 bits [M][K]; y (dev) fp32 [M][N]. */
+ql_status qlinear_mx4_gemv(int64_t M, int64_t N, int64_t K, const uint8_t *codes, const uint8_t *scales,
+                           const uint16_t *x, float *y, hipStream_t stream);
+
+/* GEMM of two MX4 operands, 1 <= M < 2^24: y[m][n] = sum_k W[n][k] * X[m][k] on the scaled matrix
+ * instructions (exact products, fp32 sums, deterministic).
+ *   x_codes, x_scales (dev) X [M][K]; codes, scales (dev) W [N][K]; y (dev) fp32 [M][N];
+ *   workspace (dev, 16-byte aligned, contents need not be zeroed) of
+ *   qlinear_mx4_gemm_workspace_bytes(M, N, K) bytes, which may be 0 (then NULL will do). */
+size_t qlinear_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+ql_status qlinear_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *x_codes, const uint8_t *x_scales,
+                           const uint8_t *codes, const uint8_t *scales, float *y, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------- mixture of experts
+ *
+ * qlinear_moe_route picks each token's experts: ids[t][j], j = 0..k-1, are the k largest logits of
+ * row t in descending order, equal logits by ascending expert, and weights[t][j] their softmax,
+ * over the chosen ones (renormalize != 0) or over all E.  Logits of -inf (masked experts) and NaN
+ * are never chosen: where fewer than k remain the id is -1 and the weight 0, so a row whose logits
+ * are all -inf (a padded token) chooses nothing.  +inf takes all weight, shared by its equals.
+ *   logits (dev) [T][E] of type dtype (ql_dtype); ids (dev) int32 [T][k]; weights (dev) fp32
+ *   [T][k]; 1 <= k <= min(E, QL_MOE_MAX_TOPK), E <= QL_MOE_MAX_EXPERTS, T < 2^30. */
+#define QL_MOE_MAX_EXPERTS 1024
+#define QL_MOE_MAX_TOPK 16
+#define QL_MOE_MAX_TOKENS 64
+ql_status qlinear_moe_route(int64_t T, int64_t E, int64_t k, int renormalize, int dtype, const void *logits,
+                            int32_t *ids, float *weights, hipStream_t stream);
+
+/* The experts' products of a mixture-of-experts layer for 1 <= T <= QL_MOE_MAX_TOKENS tokens:
+ *   y[t] = sum_j weights[t][j] * down_e (silu(gate_e x_t) * (up_e x_t)),  e = ids[t][j],
+ * silu(v) = v / (1 + exp(-v)).  Pairs whose id is outside 0..E-1 are left out (y[t] = 0 if all
+ * are); an expert may appear twice in a row.  Only the experts that some token chose are read.
+ * Products are exact and sums fp32 in a fixed order; the hidden values silu(gate) * up keep 24
+ * significant bits.  Deterministic.
+ *   x (dev) bf16 bits [T][H]; ids (dev) int32 [T][k], weights (dev) fp32 [T][k] (from
+ *   qlinear_moe_route or any other router); gate, up: MX4 stacks of E matrices [I][H], down: of E
+ *   matrices [H][I]; y (dev) fp32 [T][H]; workspace (dev, 16-byte aligned, contents need not be
+ *   zeroed) of qlinear_mx4_moe_workspace_bytes.  Calls that share a workspace must not overlap.
+ * H and I are multiples of 32, at most 2^20. */
+typedef struct {
+  int32_t E, H, I, k;
+  const int32_t *ids;         /* (dev) */
+  const float *weights;       /* (dev) */
+  const uint8_t *gate_codes;  /* (dev) [E][I][H/2] */
+  const uint8_t *gate_scales; /* (dev) [E][I][scale stride of H] */
+  const uint8_t *up_codes;    /* (dev) as gate */
+  const uint8_t *up_scales;   /* (dev) as gate */
+  const uint8_t *down_codes;  /* (dev) [E][H][I/2] */
+  const uint8_t *down_scales; /* (dev) [E][H][scale stride of I] */
+} ql_mx4_experts;
+size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
+ql_status qlinear_mx4_moe(const ql_mx4_experts *experts, int64_t T, const uint16_t *x, float *y, void *workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
 /* ---------------------------------------------------------------- 4-bit container baseline
  *
  * The summary page (onedev.kr/papers/1416, section "Premises & limits") says the
