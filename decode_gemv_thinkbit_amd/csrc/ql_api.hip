@@ -479,7 +479,8 @@ static ql_status check_mx4(int64_t N, int64_t K) {
 
 static ql_status check_mx4_product(int64_t N, int64_t K) {
   QL_TRY(check_mx4(N, K));
-  if (N >= ((int64_t)1 << 26)) return fail(QL_EINVAL, "N=%lld must be below 2^26", (long long)N);
+  if (N >= ((int64_t)1 << 26) || K > ((int64_t)1 << 24))
+    return fail(QL_EINVAL, "products need N < 2^26 and K <= 2^24 (N=%lld, K=%lld)", (long long)N, (long long)K);
   return QL_OK;
 }
 
@@ -505,17 +506,29 @@ ql_status qlinear_mx4_dequant(int64_t N, int64_t K, const uint8_t* codes, const 
   return hip_status(ql::launch_mx4_dequant(N, K, codes, scales, out_bf16 != 0, out, stream), "mx4_dequant launch");
 }
 
+size_t qlinear_mx4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || M > 16 || check_mx4_product(N, K) != QL_OK) return 0;
+  const int parts = ql::mx4_gemv_plan((int)M, (int)N, (int)K).parts;
+  return parts > 1 ? (size_t)parts * M * N * sizeof(float) : 0;
+}
+
 ql_status qlinear_mx4_gemv(int64_t M, int64_t N, int64_t K, const uint8_t* codes, const uint8_t* scales,
-                           const uint16_t* x, float* y, hipStream_t stream) {
+                           const uint16_t* x, float* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (M < 1 || M > 16) return fail(QL_EINVAL, "mx4_gemv needs 1 <= M <= 16 (M=%lld)", (long long)M);
   QL_TRY(check_mx4_product(N, K));
   QL_TRY(check_ptrs({codes, scales, x, y}));
-  return hip_status(ql::launch_mx4_gemv((int)M, (int)N, (int)K, codes, scales, x, y, stream), "mx4_gemv launch");
+  const ql::GemvPlan g = ql::mx4_gemv_plan((int)M, (int)N, (int)K);
+  const size_t need = g.parts > 1 ? (size_t)g.parts * M * N * sizeof(float) : 0;
+  if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
+  if (need) QL_TRY(check_ptrs({workspace}));
+  return hip_status(ql::launch_mx4_gemv(g, (int)M, (int)N, (int)K, codes, scales, x, y,
+                                        static_cast<float*>(workspace), stream), "mx4_gemv launch");
 }
 
 size_t qlinear_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || M >= ((int64_t)1 << 24) || check_mx4_product(N, K) != QL_OK) return 0;
-  return 0;
+  const int parts = ql::mx4_gemm_plan((int)M, (int)N, (int)K).parts;
+  return parts > 1 ? (size_t)parts * M * N * sizeof(float) : 0;
 }
 
 ql_status qlinear_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* x_codes, const uint8_t* x_scales,
@@ -524,12 +537,15 @@ ql_status qlinear_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* x_cod
   if (M < 1 || M >= ((int64_t)1 << 24)) return fail(QL_EINVAL, "mx4_gemm needs 1 <= M < 2^24 (M=%lld)", (long long)M);
   QL_TRY(check_mx4(M, K));
   QL_TRY(check_mx4_product(N, K));
+  if (M > 64 && ((M + 127) / 128) * ((N + 127) / 128) >= ((int64_t)1 << 24))
+    return fail(QL_EINVAL, "too many outputs (M=%lld, N=%lld)", (long long)M, (long long)N);
   QL_TRY(check_ptrs({x_codes, x_scales, codes, scales, y}));
-  const size_t need = qlinear_mx4_gemm_workspace_bytes(M, N, K);
+  const ql::GemmPlan g = ql::mx4_gemm_plan((int)M, (int)N, (int)K);
+  const size_t need = g.parts > 1 ? (size_t)g.parts * M * N * sizeof(float) : 0;
   if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
   if (need) QL_TRY(check_ptrs({workspace}));
-  return hip_status(ql::launch_mx4_gemm((int)M, (int)N, (int)K, x_codes, x_scales, codes, scales, y, stream),
-                    "mx4_gemm launch");
+  return hip_status(ql::launch_mx4_gemm(g, (int)M, (int)N, (int)K, x_codes, x_scales, codes, scales, y,
+                                        static_cast<float*>(workspace), stream), "mx4_gemm launch");
 }
 
 // ---------------------------------------------------------------- mixture of experts

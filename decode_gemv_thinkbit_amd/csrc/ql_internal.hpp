@@ -76,10 +76,22 @@ hipError_t launch_mx4_quantize(int64_t rows, int64_t K, int type, const void* W,
                                hipStream_t stream);
 hipError_t launch_mx4_dequant(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, bool bf16,
                               void* out, hipStream_t stream);
-hipError_t launch_mx4_gemv(int M, int N, int K, const uint8_t* codes, const uint8_t* scales, const uint16_t* x,
-                           float* y, hipStream_t stream);
-hipError_t launch_mx4_gemm(int M, int N, int K, const uint8_t* xc, const uint8_t* xs, const uint8_t* wc,
-                           const uint8_t* ws, float* y, hipStream_t stream);
+// Decode GEMV: 16-row tiles and waves per workgroup, and parts of K (over 1: sums in a workspace)
+struct GemvPlan {
+  int tiles, waves, parts;
+};
+GemvPlan mx4_stream_plan(double token_bytes, int N, int K);
+GemvPlan mx4_gemv_plan(int M, int N, int K);
+hipError_t launch_mx4_gemv(const GemvPlan& g, int M, int N, int K, const uint8_t* codes, const uint8_t* scales,
+                           const uint16_t* x, float* y, float* workspace, hipStream_t stream);
+hipError_t launch_mx4_join(int64_t n, int parts, const float* in, float* y, hipStream_t stream);
+struct GemmPlan {
+  int tiles, parts;  // the streaming kernel, as in GemvPlan (tiles > 0)
+  int tile;          // else which output tile
+};
+GemmPlan mx4_gemm_plan(int M, int N, int K);
+hipError_t launch_mx4_gemm(const GemmPlan& g, int M, int N, int K, const uint8_t* xc, const uint8_t* xs,
+                           const uint8_t* wc, const uint8_t* ws, float* y, float* workspace, hipStream_t stream);
 
 // mixture of experts (ql_moe.hip)
 hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, const void* logits, int32_t* ids,

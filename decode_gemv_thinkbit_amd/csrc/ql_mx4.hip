@@ -94,43 +94,71 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(int64_t groups, uint32
 }
 
 // ---------------------------------------------------------------- decode GEMV
-// y[m][n] = sum_k W[n][k] x[m][k]: a workgroup owns 16 rows, its waves take chunks in turn and
-// their sums are joined through LDS in wave order.
-constexpr int kGemvWaves = 8;
-
-__global__ void __launch_bounds__(kGemvWaves * 64) mx4_gemv_kernel(int M, int N, int K,
-                                                                  const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales,
-                                                                  const uint16_t* __restrict__ x,
-                                                                  float* __restrict__ y) {
-  __shared__ f32x4_t part[kGemvWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
-  const int nblk = K / kMxBlock, nchunk = (nblk + 3) / 4;
-  const int64_t n = (int64_t)blockIdx.x * 16 + r, row = n < N ? n : N - 1;  // rows past N repeat the last one
-  const uint8_t* wp = codes + row * (K / 2) + q * 16;
-  const uint8_t* sp = scales + row * mx4_scale_stride(K);
-  const uint16_t* xp = x + (int64_t)(r < M ? r : M - 1) * K + q * kMxBlock;
-  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c = wave; c < nchunk; c += kGemvWaves) {
-    const bool in = 4 * c + q < nblk;  // blocks past K are zeros on both sides
-    u32x4_t w = {0u, 0u, 0u, 0u}, a[4] = {};
-    float s = 1.0f;
-    if (in) {
-      w = ld_b128(wp + c * 64);
-      s = mx4_scale_f32((ld_b32(sp + 4 * c) >> (8 * q)) & 255u);
+// y[m][n] = sum_k W[n][k] x[m][k]: a workgroup owns R tiles of 16 rows and one of the gridDim.y parts
+// of the inputs, its waves take pairs of chunks in turn and their sums are joined through LDS in wave
+// order; parts (more than one) go to `out` = [part][M][N] for mx4_join_kernel.
+template <int R, int XP, int WAVES, bool TAIL>
+__global__ void __launch_bounds__(WAVES * 64) mx4_gemv_kernel(int M, int N, int K, const uint8_t* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales,
+                                                              const uint16_t* __restrict__ x, float* __restrict__ out) {
+  using S = Skinny<1, R, XP, 2>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
+  static_assert(S::kLds >= R * 1024, "the sums are joined in the same memory");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
+  const int last = (int)min((int64_t)16 * R, N - n0) - 1;  // rows past N repeat the last one, tokens past M too
+  S job;
+  job.codes[0] = codes + n0 * (K / 2);
+  job.scales[0] = scales + n0 * mx4_scale_stride(K);
+  job.x = reinterpret_cast<const uint8_t*>(x);
+  job.init(K, [&](int t, int i) { return min(16 * t + i, last); }, [&](int m) { return min(m, M - 1); });
+  f32x4_t acc[1][R];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = ld_b128(xp + c * kMxChunk + 8 * j);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc = mfma_bf16(a[j], mx4_bf16x8(w[j], s), acc);
-  }
-  part[wave][lane] = acc;
+  for (int t = 0; t < R; ++t) acc[0][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  job.template run<TAIL>(acc, smem + wave * S::kLds, K, (int)blockIdx.y * WAVES + wave, WAVES * (int)gridDim.y);
   __syncthreads();
-  if (wave == 0) {
-    for (int v = 1; v < kGemvWaves; ++v) acc += part[v][lane];
+  f32x4_t* part = reinterpret_cast<f32x4_t*>(smem);
+#pragma unroll
+  for (int t = 0; t < R; ++t) part[(wave * R + t) * 64 + lane] = acc[0][t];
+  __syncthreads();
+  if (wave < R) {
+    f32x4_t v = part[wave * 64 + lane];
+    for (int u = 1; u < WAVES; ++u) v += part[(u * R + wave) * 64 + lane];
+    const int64_t n = n0 + 16 * wave + r;
+    out += (int64_t)blockIdx.y * M * N;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (4 * q + i < M && n < N) y[(int64_t)(4 * q + i) * N + n] = acc[i];
+      if (4 * q + i < M && n < N) out[(int64_t)(4 * q + i) * N + n] = v[i];
+  }
+}
+
+template <int R, int XP, int WAVES>
+hipError_t gemv_as(int M, int N, int K, const uint8_t* codes, const uint8_t* scales, const uint16_t* x, int parts,
+                   float* out, hipStream_t stream) {
+  const auto kernel = K % (2 * kMxChunk) ? mx4_gemv_kernel<R, XP, WAVES, true> : mx4_gemv_kernel<R, XP, WAVES, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)parts), dim3(WAVES * 64), 0, stream,
+                     M, N, K, codes, scales, x, out);
+  return hipGetLastError();
+}
+
+template <int XP>
+hipError_t gemv_tokens(const GemvPlan& g, int M, int N, int K, const uint8_t* codes, const uint8_t* scales,
+                       const uint16_t* x, float* out, hipStream_t stream) {
+  if (g.tiles == 4) return gemv_as<4, XP, 4>(M, N, K, codes, scales, x, g.parts, out, stream);
+  if (g.tiles == 2) return gemv_as<2, XP, 4>(M, N, K, codes, scales, x, g.parts, out, stream);
+  if constexpr (XP <= 2) {
+    if (g.waves == 8) return gemv_as<1, XP, 8>(M, N, K, codes, scales, x, g.parts, out, stream);
+  }
+  return gemv_as<1, XP, 4>(M, N, K, codes, scales, x, g.parts, out, stream);
+}
+
+// y = the sum of `parts` arrays of n floats, in order
+__global__ void __launch_bounds__(256) mx4_join_kernel(int64_t n, int parts, const float* __restrict__ in,
+                                                       float* __restrict__ y) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float v = in[i];
+    for (int p = 1; p < parts; ++p) v += in[p * n + i];
+    y[i] = v;
   }
 }
 
@@ -161,11 +189,44 @@ hipError_t launch_mx4_dequant(int64_t rows, int64_t K, const uint8_t* codes, con
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_gemv(int M, int N, int K, const uint8_t* codes, const uint8_t* scales, const uint16_t* x,
-                           float* y, hipStream_t stream) {
-  hipLaunchKernelGGL(mx4_gemv_kernel, dim3((unsigned)((N + 15) / 16)), dim3(kGemvWaves * 64), 0, stream, M, N, K,
-                     codes, scales, x, y);
+hipError_t launch_mx4_join(int64_t n, int parts, const float* in, float* y, hipStream_t stream) {
+  const int64_t want = (n + 255) / 256, most = 8 * (int64_t)device_cu_count();
+  hipLaunchKernelGGL(mx4_join_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, stream, n, parts, in, y);
   return hipGetLastError();
+}
+
+// What a CU has to fetch decides: a workgroup reads 17/32 bytes of each weight of its 16 R rows and
+// token_bytes per input, the tokens over again for every workgroup.  Few rows leave CUs
+// idle, so the rows per workgroup and the parts of K are chosen together for the least bytes per CU;
+// a second launch to join parts costs about 2 us of the GPU and more of the host, 150 KB at the 35 KB/us
+// that a CU was seen to fetch.
+GemvPlan mx4_stream_plan(double token_bytes, int N, int K) {
+  const int64_t cus = device_cu_count(), pairs = (K + 2 * kMxChunk - 1) / (2 * kMxChunk);
+  GemvPlan best{1, 4, 1};
+  double least = 0.0;
+  for (int tiles = 1; tiles <= 4; tiles *= 2)
+    for (int parts = 1; parts <= 8 && (parts == 1 || pairs >= 8 * parts); ++parts) {
+      const int64_t groups = ((int64_t)N + 16 * tiles - 1) / (16 * tiles) * parts;
+      const double rounds = (double)((groups + cus - 1) / cus);
+      const double cost = rounds * (8.5 * tiles + token_bytes) * K / parts + (parts > 1 ? 150e3 : 0.0);
+      if (least == 0.0 || cost < least) least = cost, best = {tiles, groups <= cus ? 8 : 4, parts};
+    }
+  return best;
+}
+
+GemvPlan mx4_gemv_plan(int M, int N, int K) {
+  return mx4_stream_plan(M <= 2 ? 4.0 : M <= 4 ? 8.0 : M <= 8 ? 16.0 : 32.0, N, K);
+}
+
+hipError_t launch_mx4_gemv(const GemvPlan& g, int M, int N, int K, const uint8_t* codes, const uint8_t* scales,
+                           const uint16_t* x, float* y, float* workspace, hipStream_t stream) {
+  float* out = g.parts > 1 ? workspace : y;
+  const hipError_t e = M <= 2   ? gemv_tokens<1>(g, M, N, K, codes, scales, x, out, stream)
+                       : M <= 4 ? gemv_tokens<2>(g, M, N, K, codes, scales, x, out, stream)
+                       : M <= 8 ? gemv_tokens<4>(g, M, N, K, codes, scales, x, out, stream)
+                                : gemv_tokens<8>(g, M, N, K, codes, scales, x, out, stream);
+  if (e != hipSuccess || g.parts == 1) return e;
+  return launch_mx4_join((int64_t)M * N, g.parts, workspace, y, stream);
 }
 
 }  // namespace ql

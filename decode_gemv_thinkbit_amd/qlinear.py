@@ -131,7 +131,9 @@ def lib():
         L.qlinear_mx4_scale_stride.restype = i64
         L.qlinear_mx4_quantize.argtypes = [i64, i64, i32, vp, vp, vp, vp]
         L.qlinear_mx4_dequant.argtypes = [i64, i64, vp, vp, i32, vp, vp]
-        L.qlinear_mx4_gemv.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
+        L.qlinear_mx4_gemv_workspace_bytes.argtypes = [i64, i64, i64]
+        L.qlinear_mx4_gemv_workspace_bytes.restype = sz
+        L.qlinear_mx4_gemv.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]
         L.qlinear_mx4_gemm_workspace_bytes.argtypes = [i64, i64, i64]
         L.qlinear_mx4_gemm_workspace_bytes.restype = sz
         L.qlinear_mx4_gemm.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -585,13 +587,23 @@ class Mx4Tensor:
         return self.codes.numel() + self.scales.numel()
 
 
-def _launch(what: str, fn, device: torch.device, *args):
-    """Call fn(*args, stream) with the current stream of `device`, made current for the call."""
+# The current stream's handle for a device index.  Building a torch.cuda.Stream object to read it
+# takes 2.8 us of host time, more than the rest of a small call's checks together.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(fn, device: torch.device, *args):
+    """fn(*args) with `device` current (the plans behind sizes and launches ask for its CUs)."""
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _launch(what: str, fn, device: torch.device, *args):
+    """Call fn(*args, stream) on the current stream of `device`."""
+    _check(_on_device(fn, device, *args, _raw_stream(device.index)), what)
 
 
 def _mx4(t: Mx4Tensor, dims: int, device: torch.device, name: str):
@@ -651,18 +663,22 @@ def mx4_dequant(t: Mx4Tensor, out_bf16: bool = False, out: Optional[torch.Tensor
     return out
 
 
-def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [M, N] fp32 = x [M, K] bf16 times the MX4 weight transposed, M <= 16."""
     _dev(x, torch.bfloat16, "x")
     if x.dim() == 1:
         x = x.view(1, -1)
     _mx4(w, 2, x.device, "w")
     M, K = x.shape
+    N = w.N
     if K != w.K:
         raise ValueError(f"x has K={K}, weight has K={w.K}")
-    out = _result(out, (M, w.N), torch.float32, x.device)
-    _launch("mx4_gemv", lib().qlinear_mx4_gemv, x.device, M, w.N, K, w.codes.data_ptr(), w.scales.data_ptr(),
-            x.data_ptr(), out.data_ptr())
+    out = _result(out, (M, N), torch.float32, x.device)
+    need = _on_device(lib().qlinear_mx4_gemv_workspace_bytes, x.device, M, N, K)
+    workspace = _scratch(workspace, need, x.device) if need else None
+    _launch("mx4_gemv", lib().qlinear_mx4_gemv, x.device, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(),
+            x.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)
     return out
 
 
@@ -675,7 +691,7 @@ def mx4_gemm(x: Mx4Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
         raise ValueError(f"x has K={x.K}, weight has K={w.K}")
     M, N, K = x.N, w.N, w.K
     out = _result(out, (M, N), torch.float32, x.codes.device)
-    need = lib().qlinear_mx4_gemm_workspace_bytes(M, N, K)
+    need = _on_device(lib().qlinear_mx4_gemm_workspace_bytes, out.device, M, N, K)
     workspace = _scratch(workspace, need, out.device) if need else None
     _launch("mx4_gemm", lib().qlinear_mx4_gemm, out.device, M, N, K, x.codes.data_ptr(), x.scales.data_ptr(),
             w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)

@@ -398,8 +398,8 @@ ql_status qlinear_lb_gemv(const ql_littlebit *w, const uint16_t *x, float *y, vo
  *   codes  uint8 [N][K/2], the even input in the low nibble; K % 32 == 0;
  *   scales uint8 [N][qlinear_mx4_scale_stride(K)]: byte b of a row is the scale of inputs
  *          32b .. 32b+31; rows are padded to whole dwords, and what the padding holds is ignored.
- * A stack of matrices (experts) is a matrix with count*N rows.  N*K is at most 2^36 elements,
- * N below 2^26 (the products), K at most 2^26. */
+ * A stack of matrices (experts) is a matrix with count*N rows.  N*K is at most 2^36 elements
+ * and K at most 2^26; the products take N below 2^26 and K up to 2^24. */
 
 /* Element types of inputs that may come in several. */
 typedef enum { QL_F32 = 0, QL_BF16 = 1, QL_F16 = 2 } ql_dtype;
@@ -422,15 +422,19 @@ ql_status qlinear_mx4_dequant(int64_t N, int64_t K, const uint8_t *codes, const 
 
 /* Decode GEMV, 1 <= M <= 16: y[m][n] = sum_k W[n][k] * x[m][k] with W in MX4 and x in bf16.  The
  * products are exact (bf16 operands on the matrix unit), sums fp32 in a fixed order: deterministic.
- *   x (dev) bf16 bits [M][K]; y (dev) fp32 [M][N]. */
+ *   x (dev) bf16 bits [M][K]; y (dev) fp32 [M][N]; workspace (dev, 16-byte aligned, contents need not
+ *   be zeroed) of qlinear_mx4_gemv_workspace_bytes(M, N, K) bytes on the current device, the sums of
+ *   parts of K where few rows would leave CUs idle; often 0 (then NULL will do).  Calls that share a
+ *   workspace must not overlap. */
+size_t qlinear_mx4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
 ql_status qlinear_mx4_gemv(int64_t M, int64_t N, int64_t K, const uint8_t *codes, const uint8_t *scales,
-                           const uint16_t *x, float *y, hipStream_t stream);
+                           const uint16_t *x, float *y, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* GEMM of two MX4 operands, 1 <= M < 2^24: y[m][n] = sum_k W[n][k] * X[m][k] on the scaled matrix
  * instructions (exact products, fp32 sums, deterministic).
  *   x_codes, x_scales (dev) X [M][K]; codes, scales (dev) W [N][K]; y (dev) fp32 [M][N];
- *   workspace (dev, 16-byte aligned, contents need not be zeroed) of
- *   qlinear_mx4_gemm_workspace_bytes(M, N, K) bytes, which may be 0 (then NULL will do). */
+ *   workspace as for qlinear_mx4_gemv, of qlinear_mx4_gemm_workspace_bytes(M, N, K) bytes.
+ * M * N is below 2^38. */
 size_t qlinear_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 ql_status qlinear_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *x_codes, const uint8_t *x_scales,
                            const uint8_t *codes, const uint8_t *scales, float *y, void *workspace,

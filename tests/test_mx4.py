@@ -86,7 +86,10 @@ def test_product_refusals():
                                 (1, 1 << 26, 128, FAKE, FAKE, FAKE, FAKE), (1, 16, 128, ODD, FAKE, FAKE, FAKE),
                                 (1, 16, 128, FAKE, None, FAKE, FAKE), (1, 16, 128, FAKE, FAKE, ODD, FAKE),
                                 (1, 16, 128, FAKE, FAKE, FAKE, None)):
-        assert L.qlinear_mx4_gemv(M, N, K, c, s, x, y, None) == 1 and message()
+        assert L.qlinear_mx4_gemv(M, N, K, c, s, x, y, FAKE, 1 << 40, None) == 1 and message()
+    assert L.qlinear_mx4_gemv(1, 16, (1 << 24) + 32, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == 1
+    for M, N, K in ((0, 16, 128), (17, 16, 128), (1, 16, 100), (1, 0, 128)):
+        assert L.qlinear_mx4_gemv_workspace_bytes(M, N, K) == 0
     for M, N, K, p in ((0, 16, 128, FAKE), (1 << 24, 16, 128, FAKE), (16, 16, 96 + 1, FAKE), (16, 1 << 26, 32, FAKE),
                        (16, 16, 128, ODD), (16, 16, 128, None)):
         assert L.qlinear_mx4_gemm(M, N, K, FAKE, FAKE, p, FAKE, FAKE, FAKE, 1 << 40, None) == 1 and message()
