@@ -571,13 +571,13 @@ static ql_status check_moe_sizes(int64_t T, int64_t k, int64_t H, int64_t I) {
   if (T < 1 || T > QL_MOE_MAX_TOKENS)
     return fail(QL_EINVAL, "mx4_moe takes 1..%d tokens (T=%lld)", QL_MOE_MAX_TOKENS, (long long)T);
   if (k < 1 || k > QL_MOE_MAX_TOPK) return fail(QL_EINVAL, "1 <= k <= %d (k=%lld)", QL_MOE_MAX_TOPK, (long long)k);
-  if (H <= 0 || I <= 0 || H % 32 || I % 32 || H > ((int64_t)1 << 20) || I > ((int64_t)1 << 20))
-    return fail(QL_EINVAL, "H=%lld and I=%lld must be multiples of 32, at most 2^20", (long long)H, (long long)I);
+  if (H <= 0 || I <= 0 || H % 32 || I % 32 || H > ((int64_t)1 << 18) || I > ((int64_t)1 << 18))
+    return fail(QL_EINVAL, "H=%lld and I=%lld must be multiples of 32, at most 2^18", (long long)H, (long long)I);
   return QL_OK;
 }
 
-size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I) {
-  return check_moe_sizes(T, k, H, I) == QL_OK ? ql::mx4_moe_workspace_bytes(T, k, I) : 0;
+size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  return check_moe_sizes(T, k, H, I) == QL_OK && check_topk(T, E, k) == QL_OK ? ql::mx4_moe_workspace_bytes(T, k, E, H, I) : 0;
 }
 
 ql_status qlinear_mx4_moe(const ql_mx4_experts* e, int64_t T, const uint16_t* x, float* y, void* workspace,
@@ -587,7 +587,7 @@ ql_status qlinear_mx4_moe(const ql_mx4_experts* e, int64_t T, const uint16_t* x,
   QL_TRY(check_topk(T, e->E, e->k));
   QL_TRY(check_ptrs({e->ids, e->weights, e->gate_codes, e->gate_scales, e->up_codes, e->up_scales, e->down_codes,
                      e->down_scales, x, y, workspace}));
-  const size_t need = ql::mx4_moe_workspace_bytes(T, e->k, e->I);
+  const size_t need = ql::mx4_moe_workspace_bytes(T, e->k, e->E, e->H, e->I);
   if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
   const ql::MoeArgs a{(int32_t)T, e->k, e->E, e->H, e->I, x, e->ids, e->weights, e->gate_codes, e->gate_scales,
                       e->up_codes, e->up_scales, e->down_codes, e->down_scales, y, workspace};

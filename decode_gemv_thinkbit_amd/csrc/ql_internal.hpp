@@ -105,7 +105,7 @@ struct MoeArgs {
   float* y;
   void* workspace;
 };
-size_t mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t I);
+size_t mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream);
 
 int device_cu_count();

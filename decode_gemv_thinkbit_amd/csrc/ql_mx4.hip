@@ -108,14 +108,22 @@ __global__ void __launch_bounds__(WAVES * 64) mx4_gemv_kernel(int M, int N, int 
   const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
   const int last = (int)min((int64_t)16 * R, N - n0) - 1;  // rows past N repeat the last one, tokens past M too
   S job;
-  job.codes[0] = codes + n0 * (K / 2);
-  job.scales[0] = scales + n0 * mx4_scale_stride(K);
-  job.x = reinterpret_cast<const uint8_t*>(x);
-  job.init(K, [&](int t, int i) { return min(16 * t + i, last); }, [&](int m) { return min(m, M - 1); });
+  const uint8_t* const c[1] = {codes + n0 * (K / 2)};
+  const uint8_t* const s[1] = {scales + n0 * mx4_scale_stride(K)};
   f32x4_t acc[1][R];
+  bool once = true;
+  job.template run<TAIL>(
+      smem + wave * S::kLds, K, (int)blockIdx.y * WAVES + wave, WAVES * (int)gridDim.y, r < 2 * XP ? r : 0, 1,
+      [&](S& j) {
+        if (once) j.init(K, c, s, [&](int t, int i) { return min(16 * t + i, last); }, x, [&](int m) { return min(m, M - 1); });
+        const bool is = once;
+        once = false;
+        return is;
+      },
+      [&](const f32x4_t(&sums)[1][R]) {
 #pragma unroll
-  for (int t = 0; t < R; ++t) acc[0][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  job.template run<TAIL>(acc, smem + wave * S::kLds, K, (int)blockIdx.y * WAVES + wave, WAVES * (int)gridDim.y);
+        for (int t = 0; t < R; ++t) acc[0][t] = sums[0][t];
+      });
   __syncthreads();
   f32x4_t* part = reinterpret_cast<f32x4_t*>(smem);
 #pragma unroll

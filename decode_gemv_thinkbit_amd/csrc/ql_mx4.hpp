@@ -54,23 +54,46 @@ __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, bf16x8_t b, f32x4_t c) {
 }
 
 // ---------------------------------------------------------------- loads straight into LDS
-// 16 (or 4) bytes per lane: lane l's bytes land at lds + 16 l (4 l); lds is wave-uniform.  With `now`
-// false nothing is read or written, but the load still counts, so waits by count stay right and no
-// branch splits a loop's block.  The compiler does not see the write: readers wait with wait_vm (and a
-// barrier, if other waves read).  m0 is set for each load: nothing else here keeps a value in it.
+// 16 (or 4) bytes per lane: lane l's bytes land at lds + 16 l (4 l); lds is wave-uniform.  The compiler
+// does not see the write: readers wait with wait_vm (and a barrier, if other waves read).  m0 is set in
+// each block: nothing else here keeps a value in it.
 __device__ __forceinline__ void dma16(uint32_t lds, const uint8_t* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
+// With `now` false nothing is read or written, but the load still counts, so waits by count stay right and
+// no branch splits a loop's block.
 __device__ __forceinline__ void dma16_if(bool now, uint32_t lds, const uint8_t* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\t"
                "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
-               :: "s"(lds), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(now ? ~0u : 0u)) : "memory");
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform_ptr(base)),
+                  "s"(__builtin_amdgcn_readfirstlane(now ? ~0u : 0u)) : "memory");
 }
-__device__ __forceinline__ void dma4_if(bool now, uint32_t lds, const uint8_t* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\t"
-               "global_load_lds_dword %1, %2\n\ts_mov_b64 exec, -1"
-               :: "s"(lds), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(now ? ~0u : 0u)) : "memory");
+// Two pieces, to lds and lds + 1024, from base + 1024 + off0 and base + 1024 + off1 (an instruction's
+// offset moves both of its addresses); the second only with `both`.
+__device__ __forceinline__ void dma16_two(uint32_t lds, const uint8_t* base, uint32_t off0_plus_1024, uint32_t off1) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+               "global_load_lds_dwordx4 %2, %3 offset:1024"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off0_plus_1024), "v"(off1), "s"(uniform_ptr(base)) : "memory");
+}
+__device__ __forceinline__ void dma16_two_if(bool first, bool second, uint32_t lds, const uint8_t* base,
+                                             uint32_t off0_plus_1024, uint32_t off1) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
+               "global_load_lds_dwordx4 %1, %3\n\ts_mov_b32 exec_lo, %5\n\ts_mov_b32 exec_hi, %5\n\t"
+               "global_load_lds_dwordx4 %2, %3 offset:1024\n\ts_mov_b64 exec, -1"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off0_plus_1024), "v"(off1), "s"(uniform_ptr(base)),
+                  "s"(__builtin_amdgcn_readfirstlane(first ? ~0u : 0u)),
+                  "s"(__builtin_amdgcn_readfirstlane(second ? ~0u : 0u)) : "memory");
+}
+__device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* p) {  // p per lane
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
+}
+// n loads that read nothing, for the count
+template <int N>
+__device__ __forceinline__ void dma_none(uint32_t lds, const uint8_t* base) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) dma16_if(false, lds, base, 0u);
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -93,112 +116,178 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // 4q + i of row r comes out in acc[b][t][i].
 template <int NB, int R, int XP, int DEPTH>
 struct Skinny {
-  static constexpr int kTile = 2048 + 256;  // codes and scales of a tile
-  static constexpr int kStage = NB * R * kTile + XP * 1024;
+  static constexpr int kTiles = NB * R, kScaleLoads = (kTiles + 1) / 2;
+  static constexpr int kScaleAt = kTiles * 2048, kXAt = kScaleAt + kScaleLoads * 256;
+  static constexpr int kStage = kXAt + XP * 1024;
   static constexpr int kLds = DEPTH * kStage;  // per wave
-  static constexpr int kLoads = NB * R * 3 + XP;
+  static constexpr int kLoads = kTiles * 2 + kScaleLoads + XP;
   static_assert(DEPTH * kLoads < 64, "the load counter has six bits");
+  static_assert(XP == 1 || XP % 2 == 0, "");
 
-  const uint8_t *codes[NB], *scales[NB], *x;
-  uint32_t code_off[2 * R];  // the lane's row and block of each piece
-  uint32_t scale_off[R];     // the lane's row
-  uint32_t x_off[XP];        // the lane's token and granule
-  int block[2], gran[XP];
+  const uint8_t* codes[NB];           // each 1024 below its matrix
+  const uint8_t* x;                   // 1024 below the tokens (XP > 1)
+  uint32_t code_off[2 * R];           // the lane's row and block of each piece (the first of two + 1024)
+  const uint8_t* scales[kScaleLoads];  // the lane's row and dword: lanes 0..31 an even tile, 32..63 the next
+  uint32_t x_off[XP];                 // the lane's token and granule (the first of two + 1024)
+  int pieces = XP;                    // of the tokens: those past it are not loaded
 
-  // row(t, i): byte-row index (already clamped to the matrix) of row i of tile t; token(m): row index of x
+  static __device__ __forceinline__ int block(int h) {
+    const int lane = threadIdx.x & 63;
+    return (lane & 7) ^ (4 * h + (lane >> 4));
+  }
+  static __device__ __forceinline__ int gran(int i) {
+    const int lane = threadIdx.x & 63;
+    return (lane & 31) ^ ((2 * i + (lane >> 5)) & 15);
+  }
+  // c[b], s[b]: the matrices (from the tiles' first row on); row(t, i): row i of tile t in them, within
+  // the matrix; tokens: bf16 rows of K; token(m): the row of token slot m
   template <class Row, class Token>
-  __device__ __forceinline__ void init(int K, Row row, Token token) {
+  __device__ __forceinline__ void init(int K, const uint8_t* const (&c)[NB], const uint8_t* const (&s)[NB], Row row,
+                                       const void* tokens, Token token) {
     const int lane = threadIdx.x & 63;
     const uint32_t row_bytes = (uint32_t)K / 2, stride = (uint32_t)mx4_scale_stride(K);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) block[h] = (lane & 7) ^ (4 * h + (lane >> 4));
+    for (int b = 0; b < NB; ++b) codes[b] = c[b] - 1024;
 #pragma unroll
-    for (int t = 0; t < R; ++t) {
+    for (int t = 0; t < R; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) code_off[2 * t + h] = (uint32_t)row(t, 8 * h + (lane >> 3)) * row_bytes + block[h] * 16;
-      scale_off[t] = (uint32_t)row(t, (lane >> 1) & 15) * stride;
+      for (int h = 0; h < 2; ++h)
+        code_off[2 * t + h] = (uint32_t)row(t, 8 * h + (lane >> 3)) * row_bytes + block(h) * 16 + (h ? 0 : 1024);
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const int a = 2 * i, b = 2 * i + 1 < kTiles ? 2 * i + 1 : a;  // tiles in order of (matrix, tile)
+      const uint8_t* base = lane < 32 ? s[a / R] : s[b / R];
+      const int at = lane < 32 ? row(a % R, (lane >> 1) & 15) : row(b % R, (lane >> 1) & 15);
+      scales[i] = base + (uint32_t)at * stride + (lane & 1) * 4;
     }
+    x = (const uint8_t*)tokens - (XP > 1 ? 1024 : 0);
 #pragma unroll
-    for (int i = 0; i < XP; ++i) {
-      const int m = 2 * i + (lane >> 5);
-      gran[i] = (lane & 31) ^ (m & 15);
-      x_off[i] = (uint32_t)token(m) * (uint32_t)K * 2 + gran[i] * 16;
-    }
+    for (int i = 0; i < XP; ++i)
+      x_off[i] = (uint32_t)token(2 * i + (lane >> 5)) * (uint32_t)K * 2 + gran(i) * 16 + (XP > 1 && i % 2 == 0 ? 1024 : 0);
   }
 
+  // Loads pair p.  The last pair may end inside (TAIL): its blocks and granules past K repeat the last ones.
   template <bool TAIL>
   __device__ __forceinline__ void send(bool now, uint32_t lds, int K, int p) const {
-    const int lane = threadIdx.x & 63, nblk = K / kMxBlock, nchunk = (nblk + 3) / 4;
-    uint32_t at = lds;
+    const int nblk = K / kMxBlock;
+    if (!now) {
+      dma_none<kLoads>(lds, x);
+    } else if (!TAIL || 8 * p + 8 <= nblk) {  // uniform
+      send_as(lds, p, [](int) { return 0u; }, 0u, [](int) { return 0u; });
+    } else {
+      const int lane = threadIdx.x & 63, nchunk = (nblk + 3) / 4;
+      send_as(lds, p, [&](int h) { return (uint32_t)max(0, 8 * p + block(h) - (nblk - 1)) * 16; },
+              (uint32_t)max(0, 2 * p + (lane & 1) - (nchunk - 1)) * 4,
+              [&](int i) { return (uint32_t)max(0, 32 * p + gran(i) - (K / 8 - 1)) * 16; });
+    }
+  }
+  template <class Back, class XBack>
+  __device__ __forceinline__ void send_as(uint32_t lds, int p, Back back, uint32_t sback, XBack xback) const {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+        dma16_two(lds + (b * R + t) * 2048, codes[b] + (int64_t)p * 128, code_off[2 * t] - back(0), code_off[2 * t + 1] - back(1));
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) dma4(lds + kScaleAt + i * 256, scales[i] + (int64_t)p * 8 - sback);
+    if constexpr (XP == 1) dma16(__builtin_amdgcn_readfirstlane(lds + kXAt), (const uint8_t*)uniform_ptr(x + (int64_t)p * 512), x_off[0] - xback(0));
+#pragma unroll
+    for (int i = 0; i + 1 < XP; i += 2)
+      dma16_two_if(i < pieces, i + 1 < pieces, lds + kXAt + i * 1024, x + (int64_t)p * 512, x_off[i] - xback(i),
+                   x_off[i + 1] - xback(i + 1));
+  }
+
+  // Adds pair p, whose stage is at st, to acc; the stage is read when `reading` is called.  xrow: the LDS
+  // row (token slot) that the lane's operand row r comes from.
+  template <bool TAIL, class Read>
+  static __device__ __forceinline__ void multiply(f32x4_t (&acc)[NB][R], const uint8_t* st, int K, int p, int xrow,
+                                                  Read reading) {
+    const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15, nblk = K / kMxBlock;
+    u32x4_t w[NB][R][2], a[2][4];
+    u32x2_t s[NB][R];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int t = 0; t < R; ++t) {
+        const uint8_t* tile = st + (b * R + t) * 2048;
+        s[b][t] = *reinterpret_cast<const u32x2_t*>(st + kScaleAt + (b * R + t) * 128 + r * 8);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t back = TAIL ? (uint32_t)max(0, 8 * p + block[h] - (nblk - 1)) * 16 : 0u;
-          dma16_if(now, at + 1024 * h, codes[b] + (int64_t)p * 128, code_off[2 * t + h] - back);
-        }
-        dma4_if(now, at + 2048, scales[b], scale_off[t] + (uint32_t)min(2 * p + (lane & 1), nchunk - 1) * 4);
-        at += kTile;
+        for (int h = 0; h < 2; ++h)
+          w[b][t][h] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
       }
 #pragma unroll
-    for (int i = 0; i < XP; ++i) {
-      const uint32_t back = TAIL ? (uint32_t)max(0, 32 * p + gran[i] - (K / 8 - 1)) * 16 : 0u;
-      dma16_if(now, at, x + (int64_t)p * 512, x_off[i] - back);
-      at += 1024;
-    }
-  }
-
-  // smem: the wave's kLds bytes
-  template <bool TAIL>
-  __device__ __forceinline__ void run(f32x4_t (&acc)[NB][R], const uint8_t* smem, int K, int first, int step) const {
-    const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
-    const int nblk = K / kMxBlock, npair = (nblk + 7) / 8;
-    const uint32_t lds = lds_offset(smem);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) send<TAIL>(first + d * step < npair, lds + d * kStage, K, min(first + d * step, npair - 1));
-    int d = 0;
-    for (int p = first; p < npair; p += step) {
-      wait_vm<(DEPTH - 1) * kLoads>();
-      const uint8_t* st = smem + d * kStage;
-      u32x4_t w[NB][R][2], a[2][4];
-      u32x2_t s[NB][R];
+      for (int j = 0; j < 4; ++j)
+        a[h][j] = *reinterpret_cast<const u32x4_t*>(st + kXAt + xrow * 512 + (((16 * h + 4 * q + j) ^ (xrow & 15)) << 4));
+    wait_lgkm();
+    reading();
+uint32_t e[NB][R][2];  // scale bytes
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int t = 0; t < R; ++t) {
-          const uint8_t* tile = st + (b * R + t) * kTile;
-          s[b][t] = *reinterpret_cast<const u32x2_t*>(tile + 2048 + r * 8);
+      for (int t = 0; t < R; ++t)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w[b][t][h] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[h][j] = *reinterpret_cast<const u32x4_t*>(st + NB * R * kTile + (r < 2 * XP ? r : 0) * 512 +
-                                                     (((16 * h + 4 * q + j) ^ (r < 2 * XP ? r : 0)) << 4));
-      wait_lgkm();  // the stage is read: send into it
-      send<TAIL>(p + DEPTH * step < npair, lds + d * kStage, K, min(p + DEPTH * step, npair - 1));
+        for (int h = 0; h < 2; ++h) e[b][t][h] = (s[b][t][h] >> (8 * q)) & 255u;
+    if (TAIL && 8 * p + 8 > nblk) {  // blocks past K: zeros
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool in = !TAIL || 8 * p + 4 * h + q < nblk;  // blocks past K: zeros
+        const bool in = 8 * p + 4 * h + q < nblk;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (TAIL) a[h][j] = in ? a[h][j] : u32x4_t{0u, 0u, 0u, 0u};
+        for (int j = 0; j < 4; ++j) a[h][j] = in ? a[h][j] : u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int t = 0; t < R; ++t) {
-            if (TAIL) w[b][t][h] = in ? w[b][t][h] : u32x4_t{0u, 0u, 0u, 0u};
-            const float scale = in ? mx4_scale_f32((s[b][t][h] >> (8 * q)) & 255u) : 1.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[b][t] = mfma_bf16(a[h][j], mx4_bf16x8(w[b][t][h][j], scale), acc[b][t]);
+            w[b][t][h] = in ? w[b][t][h] : u32x4_t{0u, 0u, 0u, 0u};
+            e[b][t][h] = in ? e[b][t][h] : 127u;
           }
       }
-      d = d + 1 == DEPTH ? 0 : d + 1;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const float scale = mx4_scale_f32(e[b][t][h]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[b][t] = mfma_bf16(a[h][j], mx4_bf16x8(w[b][t][h][j], scale), acc[b][t]);
+        }
+  }
+
+  // The wave's whole work: a run of jobs of the same K, each over pairs first, first + step, ...; loads
+  // run DEPTH pairs ahead, into the next jobs too.  next(job) sets the loads up for the job after the last
+  // one it set up (false: no more); done(acc) takes a job's sums, in the same order, `jobs` times.
+  //   smem: the wave's kLds bytes
+  template <bool TAIL, class Next, class Done>
+  __device__ __forceinline__ void run(const uint8_t* smem, int K, int first, int step, int xrow, int jobs, Next next,
+                                      Done done) {
+    const int npair = (K / kMxBlock + 7) / 8;
+    const uint32_t lds = lds_offset(smem);
+    bool more = first < npair && next(*this);
+    int ahead = first;
+    auto produce = [&](int d) __attribute__((always_inline)) {
+      send<TAIL>(more, lds + d * kStage, K, min(ahead, npair - 1));
+      if (more) {
+        ahead += step;
+        if (ahead >= npair) ahead = first, more = next(*this);
+      }
+    };
+    for (int d = 0; d < DEPTH; ++d) produce(d);
+    int d = 0;
+    for (int job = 0; job < jobs; ++job) {
+      f32x4_t acc[NB][R];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < R; ++t) acc[b][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int p = first; p < npair; p += step) {
+        wait_vm<(DEPTH - 1) * kLoads>();
+        multiply<TAIL>(acc, smem + d * kStage, K, p, xrow, [&]() __attribute__((always_inline)) { produce(d); });
+        d = d + 1 == DEPTH ? 0 : d + 1;
+      }
+      done(acc);
     }
     wait_vm<0>();  // nothing may land in LDS after this
   }

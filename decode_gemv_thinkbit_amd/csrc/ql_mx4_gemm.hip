@@ -234,7 +234,8 @@ template <int R, int MT, bool TAIL>
 __global__ void __launch_bounds__(256) mx4_gemm_skinny_kernel(int M, int N, int K, const uint8_t* __restrict__ xc,
     const uint8_t* __restrict__ xs, const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
     float* __restrict__ out) {
-  constexpr int kWaves = 4, kTiles = R + MT, kTile = 2048 + 256, kStage = kTiles * kTile, kLoads = 3 * kTiles;
+  constexpr int kWaves = 4, kTiles = R + MT, kScaleLoads = (kTiles + 1) / 2;
+  constexpr int kScaleAt = kTiles * 2048, kStage = kScaleAt + kScaleLoads * 256, kLoads = 2 * kTiles + kScaleLoads;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kWaves * 2 * kStage];
   static_assert(2 * kStage >= R * MT * 1024 && 2 * kLoads < 64, "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
@@ -242,34 +243,48 @@ __global__ void __launch_bounds__(256) mx4_gemm_skinny_kernel(int M, int N, int 
   const uint32_t row_bytes = (uint32_t)K / 2, stride = (uint32_t)mx4_scale_stride(K);
   const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
   const int last = (int)min((int64_t)16 * R, N - n0) - 1;  // rows past the end repeat the last one
-  const uint8_t *wb = wc + n0 * row_bytes, *wsb = ws + n0 * stride;
-  uint32_t code_off[2 * kTiles], scale_off[kTiles];
+  const uint8_t* wsb = ws + n0 * stride;
+  // dma16_two's bases and offsets; scales of two tiles a load (lanes 0..31 an even tile, 32..63 the next)
+  const uint8_t *wb = wc + n0 * row_bytes - 1024, *xb = xc - 1024;
+  auto tile_row = [&](int t, int i) { return t < R ? min(16 * t + i, last) : min(16 * (t - R) + i, M - 1); };
+  uint32_t code_off[2 * kTiles];
+  const uint8_t* scales[kScaleLoads];
   int block[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) block[h] = (lane & 7) ^ (4 * h + (lane >> 4));
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int base = 16 * (t < R ? t : t - R), end = t < R ? last : M - 1;
+  for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) code_off[2 * t + h] = (uint32_t)min(base + 8 * h + (lane >> 3), end) * row_bytes + block[h] * 16;
-    scale_off[t] = (uint32_t)min(base + ((lane >> 1) & 15), end) * stride;
+    for (int h = 0; h < 2; ++h)
+      code_off[2 * t + h] = (uint32_t)tile_row(t, 8 * h + (lane >> 3)) * row_bytes + block[h] * 16 + (h ? 0 : 1024);
+#pragma unroll
+  for (int i = 0; i < kScaleLoads; ++i) {
+    const int a = 2 * i, b = 2 * i + 1 < kTiles ? 2 * i + 1 : a, row = (lane >> 1) & 15;
+    scales[i] = lane < 32 ? (a < R ? wsb : xs) + (uint32_t)tile_row(a, row) * stride
+                          : (b < R ? wsb : xs) + (uint32_t)tile_row(b, row) * stride;
+    scales[i] += (lane & 1) * 4;
   }
   const uint8_t* mine = smem + wave * 2 * kStage;
   const uint32_t lds = lds_offset(mine);
   const int step = kWaves * (int)gridDim.y, first = (int)blockIdx.y * kWaves + wave;
   auto send = [&](int p, int d) __attribute__((always_inline)) {
-    const bool now = p < npair;
-    const int pp = min(p, npair - 1);
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const uint32_t at = lds + d * kStage + t * kTile;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t back = TAIL ? (uint32_t)max(0, 8 * pp + block[h] - (nblk - 1)) * 16 : 0u;
-        dma16_if(now, at + 1024 * h, (t < R ? wb : xc) + (int64_t)pp * 128, code_off[2 * t + h] - back);
-      }
-      dma4_if(now, at + 2048, t < R ? wsb : xs, scale_off[t] + (uint32_t)min(2 * pp + (lane & 1), nchunk - 1) * 4);
+    const uint32_t at = lds + d * kStage;
+    if (p >= npair) {
+      dma_none<kLoads>(at, wc);
+      return;
     }
+    const bool tail = TAIL && 8 * p + 8 > nblk;
+    uint32_t back[2] = {0u, 0u}, sback = 0u;
+    if (tail) {
+      back[0] = (uint32_t)max(0, 8 * p + block[0] - (nblk - 1)) * 16;
+      back[1] = (uint32_t)max(0, 8 * p + block[1] - (nblk - 1)) * 16;
+      sback = (uint32_t)max(0, 2 * p + (lane & 1) - (nchunk - 1)) * 4;
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+      dma16_two(at + t * 2048, (t < R ? wb : xb) + (int64_t)p * 128, code_off[2 * t] - back[0], code_off[2 * t + 1] - back[1]);
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) dma4(at + kScaleAt + i * 256, scales[i] + (int64_t)p * 8 - sback);
   };
   f32x4_t acc[R][MT];
 #pragma unroll
@@ -285,10 +300,11 @@ __global__ void __launch_bounds__(256) mx4_gemm_skinny_kernel(int M, int N, int 
     u32x2_t s[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const uint8_t* tile = mine + d * kStage + t * kTile;
-      s[t] = *reinterpret_cast<const u32x2_t*>(tile + 2048 + r * 8);
+      const uint8_t* st = mine + d * kStage;
+      s[t] = *reinterpret_cast<const u32x2_t*>(st + kScaleAt + t * 128 + r * 8);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) c[t][h] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
+      for (int h = 0; h < 2; ++h)
+        c[t][h] = *reinterpret_cast<const u32x4_t*>(st + t * 2048 + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
     }
     wait_lgkm();  // the stage is read: send into it
     send(p + 2 * step, d);

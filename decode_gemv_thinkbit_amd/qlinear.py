@@ -138,7 +138,7 @@ def lib():
         L.qlinear_mx4_gemm_workspace_bytes.restype = sz
         L.qlinear_mx4_gemm.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
         L.qlinear_moe_route.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, vp]
-        L.qlinear_mx4_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.qlinear_mx4_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
         L.qlinear_mx4_moe_workspace_bytes.restype = sz
         L.qlinear_mx4_moe.argtypes = [vp, i64, vp, vp, vp, sz, vp]
         for name in ("qlinear_mx4_quantize", "qlinear_mx4_dequant", "qlinear_mx4_gemv", "qlinear_mx4_gemm",
@@ -741,7 +741,7 @@ def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4
     if ids.shape != (T, k) or weights.shape != (T, k) or ids.device != x.device or weights.device != x.device:
         raise ValueError(f"ids and weights must be [{T}, k] on {x.device}")
     out = _result(out, (T, H), torch.float32, x.device)
-    need = lib().qlinear_mx4_moe_workspace_bytes(T, k, H, I)
+    need = _on_device(lib().qlinear_mx4_moe_workspace_bytes, x.device, T, k, E, H, I)
     workspace = _scratch(workspace, max(need, 16), x.device)
     e = ql_mx4_experts(E, H, I, k, ids.data_ptr(), weights.data_ptr(), gate.codes.data_ptr(), gate.scales.data_ptr(),
                        up.codes.data_ptr(), up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr())

@@ -465,7 +465,7 @@ ql_status qlinear_moe_route(int64_t T, int64_t E, int64_t k, int renormalize, in
  *   qlinear_moe_route or any other router); gate, up: MX4 stacks of E matrices [I][H], down: of E
  *   matrices [H][I]; y (dev) fp32 [T][H]; workspace (dev, 16-byte aligned, contents need not be
  *   zeroed) of qlinear_mx4_moe_workspace_bytes.  Calls that share a workspace must not overlap.
- * H and I are multiples of 32, at most 2^20. */
+ * H and I are multiples of 32, at most 2^18. */
 typedef struct {
   int32_t E, H, I, k;
   const int32_t *ids;         /* (dev) */
@@ -477,7 +477,7 @@ typedef struct {
   const uint8_t *down_codes;  /* (dev) [E][H][I/2] */
   const uint8_t *down_scales; /* (dev) [E][H][scale stride of I] */
 } ql_mx4_experts;
-size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
+size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 ql_status qlinear_mx4_moe(const ql_mx4_experts *experts, int64_t T, const uint16_t *x, float *y, void *workspace,
                           size_t workspace_bytes, hipStream_t stream);
 

@@ -145,7 +145,7 @@ def test_moe_guarded_buffers(dev):
     T, E, k, H, I = 9, 12, 3, 96, 64
     experts, x = stacks(E, H, I, 6, dev), inputs(T, H, 3).to(dev)
     ids, weights = ql.moe_route(torch.randn(T, E, device=dev), k)
-    need = ql.lib().qlinear_mx4_moe_workspace_bytes(T, k, H, I)
+    need = ql.lib().qlinear_mx4_moe_workspace_bytes(T, k, E, H, I)
     ws = torch.full((256 + need + 256,), 0x5A, dtype=torch.uint8, device=dev)
     buf = torch.full((64 + T * H + 64,), 7.0, device=dev)
     y = ql.mx4_moe(x, ids, weights, *experts, out=buf[64:64 + T * H].view(T, H), workspace=ws[256:256 + need])

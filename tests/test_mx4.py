@@ -111,8 +111,8 @@ def test_moe_refusals():
         ctypes.byref(ql.ql_mx4_experts(**{**ok, **k})), T, x, y, ws, size, None)
     assert L.qlinear_mx4_moe(None, 4, FAKE, FAKE, FAKE, 1 << 30, None) == 1
     for bad in (dict(T=0), dict(T=65), dict(E=0), dict(E=1025), dict(k=0), dict(k=9), dict(E=64, k=17), dict(H=100),
-                dict(I=33), dict(H=0), dict(I=-32), dict(H=(1 << 20) + 32), dict(x=None), dict(y=ODD), dict(ws=None),
+                dict(I=33), dict(H=0), dict(I=-32), dict(H=(1 << 18) + 32), dict(x=None), dict(y=ODD), dict(ws=None),
                 dict(ids=None), dict(weights=ODD), dict(down_scales=None), dict(up_codes=ODD), dict(size=16)):
         assert call(**bad) == 1 and message(), bad
-    assert L.qlinear_mx4_moe_workspace_bytes(65, 2, 128, 64) == 0
-    assert L.qlinear_mx4_moe_workspace_bytes(4, 2, 128, 64) > 0
+    assert L.qlinear_mx4_moe_workspace_bytes(65, 2, 8, 128, 64) == 0
+    assert L.qlinear_mx4_moe_workspace_bytes(4, 2, 8, 128, 64) > 0
