@@ -13,11 +13,11 @@ namespace {
 template <int TYPE>
 __device__ __forceinline__ void load8(const void* W, int64_t i, float (&v)[8]) {
   if constexpr (TYPE == QL_F32) {
-    const u32x4_t a = ld_b128((const float*)W + i), b = ld_b128((const float*)W + i + 4);
+    const u32x4_t a = ld_b128_nt((const float*)W + i), b = ld_b128_nt((const float*)W + i + 4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(a[j]), v[4 + j] = __uint_as_float(b[j]);
   } else {
-    const u32x4_t a = ld_b128((const uint16_t*)W + i);
+    const u32x4_t a = ld_b128_nt((const uint16_t*)W + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (TYPE == QL_BF16) {
@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(int64_t groups, uint3
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xF, 0xF, true));  // lane ^ 1
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xF, 0xF, true));  // lane ^ 2
     const uint32_t e = top >> 23;
     const uint32_t s = e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
     const float scale = mx4_scale_f32(s);

@@ -34,6 +34,7 @@ __host__ __device__ inline int64_t mx4_scale_stride(int64_t K) { return (K + kMx
 
 // 16 bytes at p (global memory)
 __device__ __forceinline__ u32x4_t ld_b128(const void* p) { return *(gu32x4p)p; }
+__device__ __forceinline__ u32x4_t ld_b128_nt(const void* p) { return __builtin_nontemporal_load((gu32x4p)p); }
 __device__ __forceinline__ uint32_t ld_b32(const void* p) { return *(mx_gu32p)p; }
 
 // 2^(s - 127) as the conversions take it: the byte as a float's exponent (0 means 2^-127 to them)

@@ -8,6 +8,7 @@ exceptions.  There is no fallback: if the library is missing the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -594,11 +595,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _on_device(fn, device: torch.device, *args):
-    """fn(*args) with `device` current (the plans behind sizes and launches ask for its CUs)."""
+    """fn(*args) with `device` current."""
     if device.index == torch.cuda.current_device():
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(what: str, device: torch.device, *sizes) -> int:
+    """What a call of these sizes needs on `device` (its plan depends on the CUs)."""
+    return int(_on_device(getattr(lib(), f"qlinear_{what}_workspace_bytes"), device, *sizes))
 
 
 def _launch(what: str, fn, device: torch.device, *args):
@@ -675,7 +682,7 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
     if K != w.K:
         raise ValueError(f"x has K={K}, weight has K={w.K}")
     out = _result(out, (M, N), torch.float32, x.device)
-    need = _on_device(lib().qlinear_mx4_gemv_workspace_bytes, x.device, M, N, K)
+    need = _workspace_bytes("mx4_gemv", x.device, M, N, K)
     workspace = _scratch(workspace, need, x.device) if need else None
     _launch("mx4_gemv", lib().qlinear_mx4_gemv, x.device, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(),
             x.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)
@@ -691,7 +698,7 @@ def mx4_gemm(x: Mx4Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
         raise ValueError(f"x has K={x.K}, weight has K={w.K}")
     M, N, K = x.N, w.N, w.K
     out = _result(out, (M, N), torch.float32, x.codes.device)
-    need = _on_device(lib().qlinear_mx4_gemm_workspace_bytes, out.device, M, N, K)
+    need = _workspace_bytes("mx4_gemm", out.device, M, N, K)
     workspace = _scratch(workspace, need, out.device) if need else None
     _launch("mx4_gemm", lib().qlinear_mx4_gemm, out.device, M, N, K, x.codes.data_ptr(), x.scales.data_ptr(),
             w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)
@@ -741,7 +748,7 @@ def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4
     if ids.shape != (T, k) or weights.shape != (T, k) or ids.device != x.device or weights.device != x.device:
         raise ValueError(f"ids and weights must be [{T}, k] on {x.device}")
     out = _result(out, (T, H), torch.float32, x.device)
-    need = _on_device(lib().qlinear_mx4_moe_workspace_bytes, x.device, T, k, E, H, I)
+    need = _workspace_bytes("mx4_moe", x.device, T, k, E, H, I)
     workspace = _scratch(workspace, max(need, 16), x.device)
     e = ql_mx4_experts(E, H, I, k, ids.data_ptr(), weights.data_ptr(), gate.codes.data_ptr(), gate.scales.data_ptr(),
                        up.codes.data_ptr(), up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr())
