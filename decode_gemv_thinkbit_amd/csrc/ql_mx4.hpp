@@ -57,7 +57,11 @@ __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, bf16x8_t b, f32x4_t c) {
 // ---------------------------------------------------------------- loads straight into LDS
 // 16 (or 4) bytes per lane: lane l's bytes land at lds + 16 l (4 l); lds is wave-uniform.  The compiler
 // does not see the write: readers wait with wait_vm (and a barrier, if other waves read).  m0 is set in
-// each block: nothing else here keeps a value in it.
+// each block: nothing else here keeps a value in it.  Wait states the compiler does not count inside these
+// blocks: one between a write of m0 and the load, five between a vector instruction's write of a scalar
+// register (a lane read of an address) and a load that uses it.
+
+// base computed by scalar instructions (a test reads the assembly for it)
 __device__ __forceinline__ void dma16(uint32_t lds, const uint8_t* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(lds), "v"(off), "s"(base) : "memory");
@@ -65,21 +69,21 @@ __device__ __forceinline__ void dma16(uint32_t lds, const uint8_t* base, uint32_
 // With `now` false nothing is read or written, but the load still counts, so waits by count stay right and
 // no branch splits a loop's block.
 __device__ __forceinline__ void dma16_if(bool now, uint32_t lds, const uint8_t* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\t"
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_nop 1\n\t"
                "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform_ptr(base)),
                   "s"(__builtin_amdgcn_readfirstlane(now ? ~0u : 0u)) : "memory");
 }
 // Two pieces, to lds and lds + 1024, from base + 1024 + off0 and base + 1024 + off1 (an instruction's
-// offset moves both of its addresses); the second only with `both`.
+// offset moves both of its addresses); each only if asked for.
 __device__ __forceinline__ void dma16_two(uint32_t lds, const uint8_t* base, uint32_t off0_plus_1024, uint32_t off1) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
                "global_load_lds_dwordx4 %2, %3 offset:1024"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off0_plus_1024), "v"(off1), "s"(uniform_ptr(base)) : "memory");
 }
 __device__ __forceinline__ void dma16_two_if(bool first, bool second, uint32_t lds, const uint8_t* base,
                                              uint32_t off0_plus_1024, uint32_t off1) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\ts_nop 1\n\t"
                "global_load_lds_dwordx4 %1, %3\n\ts_mov_b32 exec_lo, %5\n\ts_mov_b32 exec_hi, %5\n\t"
                "global_load_lds_dwordx4 %2, %3 offset:1024\n\ts_mov_b64 exec, -1"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off0_plus_1024), "v"(off1), "s"(uniform_ptr(base)),
@@ -126,7 +130,7 @@ struct Skinny {
   static_assert(XP == 1 || XP % 2 == 0, "");
 
   const uint8_t* codes[NB];           // each 1024 below its matrix
-  const uint8_t* x;                   // 1024 below the tokens (XP > 1)
+  const uint8_t* x = nullptr;         // 1024 below the tokens (XP > 1)
   uint32_t code_off[2 * R];           // the lane's row and block of each piece (the first of two + 1024)
   const uint8_t* scales[kScaleLoads];  // the lane's row and dword: lanes 0..31 an even tile, 32..63 the next
   uint32_t x_off[XP];                 // the lane's token and granule (the first of two + 1024)
@@ -191,7 +195,7 @@ struct Skinny {
         dma16_two(lds + (b * R + t) * 2048, codes[b] + (int64_t)p * 128, code_off[2 * t] - back(0), code_off[2 * t + 1] - back(1));
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i) dma4(lds + kScaleAt + i * 256, scales[i] + (int64_t)p * 8 - sback);
-    if constexpr (XP == 1) dma16(__builtin_amdgcn_readfirstlane(lds + kXAt), (const uint8_t*)uniform_ptr(x + (int64_t)p * 512), x_off[0] - xback(0));
+    if constexpr (XP == 1) dma16_if(true, lds + kXAt, x + (int64_t)p * 512, x_off[0] - xback(0));
 #pragma unroll
     for (int i = 0; i + 1 < XP; i += 2)
       dma16_two_if(i < pieces, i + 1 < pieces, lds + kXAt + i * 1024, x + (int64_t)p * 512, x_off[i] - xback(i),
