@@ -548,7 +548,7 @@ MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS = 1024, 16, 64  # QL_MOE_MAX_*
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # ql_dtype
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Mx4Tensor:
     """A matrix [N, K], or a stack of matrices [count, N, K], of microscaled 4-bit floats: e2m1 codes,
     two per byte with the even input in the low nibble, and one scale byte s (2^(s - 127)) per 32
@@ -562,25 +562,22 @@ class Mx4Tensor:
             raise ValueError(f"codes and scales must be torch.uint8, got {c.dtype} and {s.dtype}")
         if not (c.is_contiguous() and s.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        cs, ss = c.shape, s.shape
-        if len(cs) not in (2, 3) or cs[-1] % 16 or 0 in cs:
-            raise ValueError(f"codes must be [N, K/2] or [count, N, K/2] with K a multiple of 32, got {tuple(cs)}")
-        if ss != cs[:-1] + (4 * ((cs[-1] + 63) // 64),):
-            raise ValueError(f"scales of codes {tuple(cs)} must be [..., N, 4 * ceil(K/128)], got {tuple(ss)}")
+        *rows, half = c.shape
+        if len(rows) not in (1, 2) or half % 16 or not c.numel():
+            raise ValueError(f"codes must be [N, K/2] or [count, N, K/2] with K a multiple of 32, got {tuple(c.shape)}")
+        if [*s.shape] != [*rows, (half + 63) // 64 * 4]:
+            raise ValueError(f"scales of codes {tuple(c.shape)} must be [..., N, 4 * ceil(K/128)], got {tuple(s.shape)}")
         if c.device != s.device:
             raise ValueError("codes and scales must be on one device")
+        object.__setattr__(self, "shape", (*rows, 2 * half))  # of the values
 
     @property
     def N(self) -> int:
-        return self.codes.shape[-2]
+        return self.shape[-2]
 
     @property
     def K(self) -> int:
-        return 2 * self.codes.shape[-1]
-
-    @property
-    def shape(self) -> tuple:
-        return (*self.codes.shape[:-1], self.K)
+        return self.shape[-1]
 
     @property
     def nbytes(self) -> int:
@@ -616,9 +613,9 @@ def _launch(what: str, fn, device: torch.device, *args):
 def _mx4(t: Mx4Tensor, dims: int, device: torch.device, name: str):
     if not isinstance(t, Mx4Tensor):
         raise ValueError(f"{name} must be an Mx4Tensor")
-    if t.codes.dim() != dims:
+    if len(t.shape) != dims:
         raise ValueError(f"{name} must be {'a matrix' if dims == 2 else 'a stack of matrices'}, got {t.shape}")
-    if t.codes.device != device or not t.codes.is_cuda:
+    if t.codes.device != device or device.type != "cuda":
         raise ValueError(f"{name} must be on the device of the other operands, a CUDA (HIP) device")
     return t
 
@@ -654,7 +651,7 @@ def mx4_quantize(W: torch.Tensor, out: Optional[Mx4Tensor] = None) -> Mx4Tensor:
     if out is None:
         out = Mx4Tensor(torch.empty((*rows, K // 2), dtype=torch.uint8, device=W.device),
                         torch.empty((*rows, 4 * ((K + 127) // 128)), dtype=torch.uint8, device=W.device))
-    elif _mx4(out, W.dim(), W.device, "out").shape != tuple(W.shape):
+    elif _mx4(out, W.dim(), W.device, "out").shape != W.shape:
         raise ValueError(f"out must be {tuple(W.shape)}")
     _launch("mx4_quantize", lib().qlinear_mx4_quantize, W.device, W.numel() // K, K, _DTYPES[W.dtype], W.data_ptr(),
             out.codes.data_ptr(), out.scales.data_ptr())
@@ -663,7 +660,7 @@ def mx4_quantize(W: torch.Tensor, out: Optional[Mx4Tensor] = None) -> Mx4Tensor:
 
 def mx4_dequant(t: Mx4Tensor, out_bf16: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of an MX4 tensor, fp32 or bf16 (exact in both)."""
-    _mx4(t, t.codes.dim(), t.codes.device, "t")
+    _mx4(t, len(t.shape), t.codes.device, "t")
     out = _result(out, t.shape, torch.bfloat16 if out_bf16 else torch.float32, t.codes.device)
     _launch("mx4_dequant", lib().qlinear_mx4_dequant, out.device, out.numel() // t.K, t.K, t.codes.data_ptr(),
             t.scales.data_ptr(), 1 if out_bf16 else 0, out.data_ptr())
@@ -739,20 +736,22 @@ def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4
         raise ValueError("x must be [T, H], ids and weights [T, k]")
     T, H = x.shape
     k = ids.shape[1]
-    for t, name in ((gate, "gate"), (up, "up"), (down, "down")):
-        _mx4(t, 3, x.device, name)
-    E, I, _ = gate.shape
-    if gate.K != H or up.shape != gate.shape or down.shape != (E, H, I):
+    _mx4(gate, 3, x.device, "gate")
+    _mx4(up, 3, x.device, "up")
+    _mx4(down, 3, x.device, "down")
+    E, I, inner = gate.shape
+    if inner != H or up.shape != gate.shape or down.shape != (E, H, I):
         raise ValueError(f"x [T, {H}] needs gate and up [E, I, {H}] and down [E, {H}, I], got {gate.shape}, "
                          f"{up.shape}, {down.shape}")
-    if ids.shape != (T, k) or weights.shape != (T, k) or ids.device != x.device or weights.device != x.device:
-        raise ValueError(f"ids and weights must be [{T}, k] on {x.device}")
-    out = _result(out, (T, H), torch.float32, x.device)
-    need = _workspace_bytes("mx4_moe", x.device, T, k, E, H, I)
-    workspace = _scratch(workspace, max(need, 16), x.device)
+    device = x.device
+    if ids.shape[0] != T or weights.shape != ids.shape or ids.device != device or weights.device != device:
+        raise ValueError(f"ids and weights must be [{T}, k] on {device}")
+    out = _result(out, (T, H), torch.float32, device)
+    need = _workspace_bytes("mx4_moe", device, T, k, E, H, I)
+    workspace = _scratch(workspace, max(need, 16), device)
     e = ql_mx4_experts(E, H, I, k, ids.data_ptr(), weights.data_ptr(), gate.codes.data_ptr(), gate.scales.data_ptr(),
                        up.codes.data_ptr(), up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr())
-    _launch("mx4_moe", lib().qlinear_mx4_moe, x.device, ctypes.byref(e), T, x.data_ptr(), out.data_ptr(),
+    _launch("mx4_moe", lib().qlinear_mx4_moe, device, ctypes.byref(e), T, x.data_ptr(), out.data_ptr(),
             workspace.data_ptr(), need)
     return out
 

@@ -49,6 +49,8 @@ def test_tensor_refusals():
     t = ql.Mx4Tensor(u8(5, 80), u8(5, 8))
     assert (t.N, t.K, t.shape, t.nbytes) == (5, 160, (5, 160), 440)
     assert ql.Mx4Tensor(u8(3, 5, 16), u8(3, 5, 4)).shape == (3, 5, 32)
+    with pytest.raises(AttributeError):  # its shape was checked
+        t.codes = u8(9, 80)
     for codes, scales in ((u8(5, 80), u8(5, 5)), (u8(5, 80), u8(4, 8)), (u8(5, 24), u8(5, 4)), (u8(80), u8(8)),
                           (u8(0, 16), u8(0, 4)), (u8(80, 5).t(), u8(5, 8)), (u8(5, 16).float(), u8(5, 4)),
                           (u8(5, 16), u8(5, 4).to(torch.int8)), (u8(2, 2, 2, 16), u8(2, 2, 2, 4))):
@@ -97,7 +99,7 @@ def test_product_refusals():
 
 def test_route_refusals():
     L = ql.lib()
-    for T, E, k, ty, p in ((0, 8, 2, 0, FAKE), (1 << 30, 8, 2, 0, FAKE), (4, 0, 1, 0, FAKE), (4, 1025, 2, 0, FAKE),
+    for T, E, k, ty, p in ((0, 8, 2, 0, FAKE), (1 << 26, 8, 2, 0, FAKE), (4, 0, 1, 0, FAKE), (4, 1025, 2, 0, FAKE),
                            (4, 8, 0, 0, FAKE), (4, 8, 9, 0, FAKE), (4, 64, 17, 0, FAKE), (4, 8, 2, 5, FAKE),
                            (4, 8, 2, 0, ODD), (4, 8, 2, 0, None)):
         assert L.qlinear_moe_route(T, E, k, 1, ty, p, FAKE, FAKE, None) == 1 and message()
