@@ -105,16 +105,16 @@ __global__ void __launch_bounds__(256) moe_route_kernel(int64_t T, int E, int k,
 // to G, which share a read of its matrices.  Every workgroup finds them itself from the ids, into LDS: up
 // to 64 pairs in registers, every wave for itself; more by counting, with four barriers.
 constexpr int kMaxPairs = QL_MOE_MAX_TOKENS * QL_MOE_MAX_TOPK;
+static_assert(kMaxPairs <= 1024 && QL_MOE_MAX_TOKENS <= 64 && QL_MOE_MAX_EXPERTS <= 1024, "records of 10, 6 and 10 bits");
 constexpr int kFewPairs = 256;  // three workgroups of the gate and up kernel fit a CU's LDS, not two
 
-template <int PAIRS, int G, bool WEIGHTS>  // PAIRS: 64, or the most there may be
+template <int PAIRS, int G>  // PAIRS: 64, or the most there may be
 struct Groups {
   static constexpr bool SMALL = PAIRS == 64;
   static constexpr int kSlots = SMALL ? 64 * G : PAIRS;
   struct Storage {
-    uint32_t group[PAIRS];               // expert, pairs << 10, first slot << 16
-    uint32_t pair[kSlots];                   // pair, token << 16
-    float weight[WEIGHTS ? kSlots : 1];      // its weight
+    uint32_t group[PAIRS];  // expert, pairs << 10, first slot << 16
+    uint16_t pair[kSlots];  // pair, token << 10
     int groups;
   };
   struct Scratch {  // while finding (SMALL: not used); afterwards the memory is the caller's again
@@ -131,14 +131,12 @@ struct Groups {
     }
     return is ? like : 0;
   }
-  // All threads; returns the number of groups.  weights: of the pairs (WEIGHTS).
-  static __device__ int find(int P, int E, int k, const int32_t* __restrict__ ids, const float* __restrict__ weights,
-                             Storage& st, uint8_t* scratch) {
+  // All threads; returns the number of groups.
+  static __device__ int find(int P, int E, int k, const int32_t* __restrict__ ids, Storage& st, uint8_t* scratch) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t below = (1ull << lane) - 1;
     if constexpr (SMALL) {
       const int raw = lane < P ? ids[lane] : -1, id = raw < E ? raw : -1;  // negative: none
-      const float w = WEIGHTS && lane < P ? weights[lane] : 0.0f;
       const uint64_t like = same(id, id >= 0, E);
       const int rank = __popcll(like & below), r0 = rank - rank % G;
       uint64_t from = like;  // the group's pairs and those behind it
@@ -147,8 +145,7 @@ struct Groups {
       const uint64_t firsts = __ballot(id >= 0 && rank == r0);
       const int group = __popcll(firsts & ((1ull << lead) - 1));
       if (id >= 0) {
-        st.pair[group * G + rank % G] = (uint32_t)lane | (uint32_t)(lane / k) << 16;
-        if (WEIGHTS) st.weight[group * G + rank % G] = w;
+        st.pair[group * G + rank % G] = (uint16_t)(lane | lane / k << 10);
         if (rank % G == 0) st.group[group] = (uint32_t)id | (uint32_t)size << 10 | (uint32_t)(group * G) << 16;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // every wave reads what it wrote
@@ -192,8 +189,7 @@ struct Groups {
         const int e = sc.id[p], rank = sc.rank[p];
         if (e == 65535) continue;
         const int slot = (int)(sc.start[e] & 0xFFFF) + rank, group = (int)(sc.start[e] >> 16) + rank / G;
-        st.pair[slot] = (uint32_t)p | (uint32_t)(p / k) << 16;
-        if (WEIGHTS) st.weight[slot] = weights[p];
+        st.pair[slot] = (uint16_t)(p | p / k << 10);
         if (rank % G == 0)
           st.group[group] = (uint32_t)e | (uint32_t)min(G, (int)sc.count[e] - rank) << 10 | (uint32_t)slot << 16;
       }
@@ -212,6 +208,15 @@ struct Group {
   }
 };
 
+// A wave's first task: the first waves of all workgroups, then the second ones, ..., so that a last, partly
+// filled round loads every CU alike.  Workgroups go round the XCDs: those of one XCD take neighbouring
+// tasks, whose rows meet in a cache line where their bytes are no multiple of 128 (gate and up of 128 x 736 x
+// 2080, 6 for 24 tokens: 37.5 us without, 34.0 with; 43.9 with neighbours in one workgroup).
+__device__ __forceinline__ int first_task(int wave) {
+  const int grid = (int)gridDim.x, block = (int)blockIdx.x;
+  return wave * grid + (grid % 8 ? block : block % 8 * (grid / 8) + block / 8);
+}
+
 // The three bf16 planes of an fp32 value: hi + mid + lo == v to 24 bits (the second product then
 // runs on exact bf16 operands); of a value that is not finite only the first is kept.
 __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
@@ -226,22 +231,21 @@ __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
 // rows of both for one group.  JOIN (few tasks): workgroups take tasks in turn, the inputs' pairs of
 // chunks dealt to the four waves and their sums joined in wave order; else every wave takes tasks of its
 // own.  Either way the next task's loads are under way while one ends.
-template <int XP, bool JOIN, bool SMALL, bool TAIL>
-__global__ void __launch_bounds__(256) moe_gate_up_kernel(int T, int k, int E, int H, int I,
+template <int XP, int WAVES, bool JOIN, bool SMALL, bool TAIL>
+__global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, int E, int H, int I,
     const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint8_t* __restrict__ gc,
     const uint8_t* __restrict__ gs, const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
-    uint16_t* __restrict__ h, uint32_t* __restrict__ counters, int ncounters) {
+    uint16_t* __restrict__ h) {
   constexpr int G = 2 * XP, kPairs = SMALL ? 64 : XP == 2 ? kFewPairs : kMaxPairs;
   using S = Skinny<2, 1, XP, 2>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * S::kLds];
-  __shared__ typename Groups<kPairs, G, false>::Storage plan;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
+  __shared__ typename Groups<kPairs, G>::Storage plan;
   __shared__ f32x4_t part[JOIN ? 2 : 1][JOIN ? 4 : 1][2][64];
+  static_assert(!JOIN || WAVES == 4, "wave i finishes row i of every quarter");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
   const int P = T * k, tiles = (I + 15) / 16;
-  // the second kernel's counters start at zero
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < ncounters; i += gridDim.x * 256) counters[i] = 0u;
-  const int tasks = Groups<kPairs, G, false>::find(P, E, k, ids, nullptr, plan, smem) * tiles;
-  const int first = JOIN ? (int)blockIdx.x : 4 * (int)blockIdx.x + wave, step = (JOIN ? 1 : 4) * (int)gridDim.x;
+  const int tasks = Groups<kPairs, G>::find(P, E, k, ids, plan, smem) * tiles;
+  const int first = JOIN ? (int)blockIdx.x : first_task(wave), step = (JOIN ? 1 : WAVES) * (int)gridDim.x;
   const int mine = tasks > first ? (tasks - 1 - first) / step + 1 : 0;
   S job;
   int ahead = first, now = first;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(256) moe_gate_up_kernel(int T, int k, int E, i
     if (slot < gr.count && n < I) {
       uint16_t hv[3];
       split3(g / (1.0f + expf(-g)) * u, hv);
-      const int64_t at = (int64_t)(plan.pair[gr.first + slot] & 0xFFFFu) * I + n;
+      const int64_t at = (int64_t)(plan.pair[gr.first + slot] & 1023) * I + n;
 #pragma unroll
       for (int z = 0; z < 3; ++z) h[z * (int64_t)P * I + at] = hv[z];
     }
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(256) moe_gate_up_kernel(int T, int k, int E, i
         const uint8_t* const s[2] = {gs + row * mx4_scale_stride(H), us + row * mx4_scale_stride(H)};
         j.pieces = (gr.count + 1) / 2;
         j.init(H, c, s, [&](int, int i) { return min(i, last); }, x,
-               [&](int m) { return (int)(plan.pair[gr.first + min(m, gr.count - 1)] >> 16); });
+               [&](int m) { return plan.pair[gr.first + min(m, gr.count - 1)] >> 10; });
         ahead += step;
         return true;
       },
@@ -290,97 +294,127 @@ __global__ void __launch_bounds__(256) moe_gate_up_kernel(int T, int k, int E, i
       });
 }
 
-// y[t][n] = sum_j w[t][j] (down row n on h[t * k + j]).  A workgroup owns R tiles of 16 rows
-// (blockIdx.x) and every gridDim.y-th lot of WAVES groups; its waves take one group after another, and
-// each adds its products, times their weights, to token sums of its own in LDS, which are joined in wave
-// order.  Row 4s + z of the matrix operand is plane z of pair s (LDS row 3s + z), so the planes' sums meet
-// in one lane.  Where gridDim.y > 1, the workgroups of a tile leave their sums in `sums`
-// [gridDim.y][T][H] at device scope, and the one that counts in last adds them up in order.
-template <int R, int XP, int DEPTH, int WAVES, int TOKENS, bool SMALL, bool TAIL>
+// The down projection's operand: row 4s + z of the matrix instruction is plane z of a group's pair s (LDS row
+// 3s + z), so the planes' sums meet in one lane, smallest first.
+template <int XP>
+__device__ __forceinline__ int plane_row(int r) { return min(3 * (r >> 2) + min(r & 3, 2), 2 * XP - 1); }
+__device__ __forceinline__ float planes(const f32x4_t& v) { return (v[2] + v[1]) + v[0]; }
+
+// products[p][n] = down row n on h[p].  A task is R tiles of 16 rows for one group; every wave takes tasks of
+// its own.
+template <int R, int XP, int WAVES, int PAIRS, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int E, int H, int I,
-    const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const float* __restrict__ weights,
-    const uint8_t* __restrict__ dc, const uint8_t* __restrict__ ds, float* __restrict__ y, float* __restrict__ sums,
-    uint32_t* __restrict__ counters) {
-  constexpr int G = 2 * XP / 3, kCols = 16 * R;
+    const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint8_t* __restrict__ dc,
+    const uint8_t* __restrict__ ds, float* __restrict__ products) {
+  constexpr int G = 2 * XP / 3;
   static_assert(G <= 4, "");
-  using S = Skinny<1, R, XP, DEPTH>;
+  using S = Skinny<1, R, XP, 2>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
-  __shared__ typename Groups<SMALL ? 64 : kMaxPairs, G, true>::Storage plan;
-  __shared__ float ysum[WAVES][TOKENS][kCols];
-  __shared__ int done;
+  __shared__ typename Groups<PAIRS, G>::Storage plan;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
-  const int P = T * k;
-  for (int i = lane; i < T * kCols; i += 64) (&ysum[wave][0][0])[i] = 0.0f;
-  const int groups = Groups<SMALL ? 64 : kMaxPairs, G, true>::find(P, E, k, ids, weights, plan, smem);
-  const int n0 = blockIdx.x * kCols, last = min(kCols, H - n0) - 1;
-  const int first = (int)blockIdx.y * WAVES + wave, step = WAVES * (int)gridDim.y;
-  const int mine = groups > first ? (groups - 1 - first) / step + 1 : 0;
+  const int P = T * k, tiles = (H + 16 * R - 1) / (16 * R);
+  const int tasks = Groups<PAIRS, G>::find(P, E, k, ids, plan, smem) * tiles;
+  const int first = first_task(wave), step = WAVES * (int)gridDim.x;
+  const int mine = tasks > first ? (tasks - 1 - first) / step + 1 : 0;
   S job;
   int ahead = first, now = first;
   job.template run<TAIL>(
-      smem + wave * S::kLds, I, 0, 1, min(3 * (r >> 2) + min(r & 3, 2), 2 * XP - 1), mine,
+      smem + wave * S::kLds, I, 0, 1, plane_row<XP>(r), mine,
       [&](S& j) {
-        if (ahead >= groups) return false;
-        const Group gr(plan.group[ahead]);
+        if (ahead >= tasks) return false;
+        const Group gr(plan.group[ahead / tiles]);
+        const int n0 = ahead % tiles * (16 * R), last = min(16 * R, H - n0) - 1;
         const int64_t row = (int64_t)gr.expert * H + n0;
         const uint8_t* const c[1] = {dc + row * (I / 2)};
         const uint8_t* const s[1] = {ds + row * mx4_scale_stride(I)};
         j.pieces = (3 * gr.count + 1) / 2;
         j.init(I, c, s, [&](int t, int i) { return min(16 * t + i, last); }, h,
-               [&](int m) { return m % 3 * P + (int)(plan.pair[gr.first + min(m / 3, gr.count - 1)] & 0xFFFFu); });
+               [&](int m) { return m % 3 * P + (plan.pair[gr.first + min(m / 3, gr.count - 1)] & 1023); });
         ahead += step;
         return true;
       },
       [&](const f32x4_t(&acc)[1][R]) {
-        const Group gr(plan.group[now]);
-        const int at = gr.first + min(q, gr.count - 1), token = (int)(plan.pair[at] >> 16);
-        const float w = plan.weight[at];
-        // one quarter of the wave at a time: a token may hold the same expert twice
-        for (int z = 0; z < gr.count; ++z) {
-          if (q == z) {
+        const Group gr(plan.group[now / tiles]);
+        const int n = now % tiles * (16 * R) + r;
+        if (q < gr.count) {
+          float* out = products + (int64_t)(plan.pair[gr.first + q] & 1023) * H + n;
 #pragma unroll
-            for (int t = 0; t < R; ++t) ysum[wave][token][16 * t + r] += w * ((acc[0][t][2] + acc[0][t][1]) + acc[0][t][0]);
-          }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          for (int t = 0; t < R; ++t)
+            if (n + 16 * t < H) out[16 * t] = planes(acc[0][t]);
         }
         now += step;
       });
-  __syncthreads();
-  const bool split = gridDim.y > 1;
-  for (int i = threadIdx.x; i < T * kCols; i += WAVES * 64) {
-    const int t = i / kCols, c = i % kCols;
-    float s = ysum[0][t][c];
+}
+
+// y[t][n] = sum_j weights[t][j] products[t * k + j][n], over the pairs with an expert, in order of j: four
+// outputs a thread.
+__global__ void __launch_bounds__(256) moe_join_kernel(int T, int k, int E, int H, const int32_t* __restrict__ ids,
+                                                       const float* __restrict__ weights,
+                                                       const float* __restrict__ products, float* __restrict__ y) {
+  const int t = blockIdx.y, n = 4 * (int)(blockIdx.x * 256 + threadIdx.x);
+  if (n >= H) return;
+  f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    f32x4_t v[8];
 #pragma unroll
-    for (int v = 1; v < WAVES; ++v) s += ysum[v][t][c];
-    if (c <= last) {
-      if (split)
-        __hip_atomic_store(sums + ((int64_t)blockIdx.y * T + t) * H + n0 + c, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      else
-        y[(int64_t)t * H + n0 + c] = s;
+    for (int j = 0; j < 8; ++j)  // pairs without an expert hold nothing: read, for one round of loads, and left out
+      v[j] = *reinterpret_cast<const f32x4_t*>(products + ((int64_t)t * k + min(j0 + j, k - 1)) * H + n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int p = t * k + min(j0 + j, k - 1), id = ids[p];
+      const float w = weights[p];
+      const bool is = j0 + j < k && id >= 0 && id < E;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += is ? w * v[j][i] : 0.0f;
     }
   }
-  if (!split) return;
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are out
+  *reinterpret_cast<f32x4_t*>(y + (int64_t)t * H + n) = sum;
+}
+
+// One token: its experts (at most 16) fill the waves of one workgroup per 16 rows, whose sums are joined in
+// wave order; no second pass.
+template <bool TAIL>
+__global__ void __launch_bounds__(512) moe_down_one_kernel(int k, int E, int H, int I, const uint16_t* __restrict__ h,
+    const int32_t* __restrict__ ids, const float* __restrict__ weights, const uint8_t* __restrict__ dc,
+    const uint8_t* __restrict__ ds, float* __restrict__ y) {
+  using S = Skinny<1, 1, 2, 4>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * S::kLds];
+  __shared__ float part[8][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15;
+  const int n0 = blockIdx.x * 16;
+  const int id = lane < k ? ids[lane] : -1;
+  const float weight = lane < k ? weights[lane] : 0.0f;
+  uint64_t left = __ballot(id >= 0 && id < E);  // the pairs to load yet, then those to add yet
+  for (int i = 0; i < wave; ++i) left &= left - 1;
+  uint64_t open = left;
+  auto take = [](uint64_t& v) __attribute__((always_inline)) {  // the next pair of this wave
+    const int p = __builtin_ctzll(v);
+    for (int i = 0; i < 8; ++i) v &= v - 1;
+    return p;
+  };
+  float sum = 0.0f;
+  S job;
+  job.template run<TAIL>(
+      smem + wave * S::kLds, I, 0, 1, plane_row<2>(r), ((int)__popcll(left) + 7) / 8,
+      [&](S& j) {
+        if (!left) return false;
+        const int p = take(left);
+        const int64_t row = (int64_t)__builtin_amdgcn_readlane(id, p) * H + n0;
+        const uint8_t* const c[1] = {dc + row * (I / 2)};
+        const uint8_t* const s[1] = {ds + row * mx4_scale_stride(I)};
+        j.init(I, c, s, [](int, int i) { return i; }, h, [&](int m) { return min(m, 2) * k + p; });
+        return true;
+      },
+      [&](const f32x4_t(&acc)[1][1]) {
+        sum += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), take(open))) * planes(acc[0][0]);
+      });
+  if (lane < 16) part[wave][r] = sum;
   __syncthreads();
-  if (threadIdx.x == 0)
-    done = __hip_atomic_fetch_add(counters + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.y - 1;
-  __syncthreads();
-  if (!done) return;
-  for (int i = threadIdx.x; i < T * kCols; i += WAVES * 64) {
-    const int t = i / kCols, c = i % kCols;
-    if (c > last) continue;
-    float s = 0.0f;
-    for (int v0 = 0; v0 < (int)gridDim.y; v0 += 8) {
-      float some[8];
+  if (threadIdx.x < 16) {
+    float v = part[0][r];
 #pragma unroll
-      for (int v = 0; v < 8; ++v)
-        some[v] = v0 + v < (int)gridDim.y ? __hip_atomic_load(sums + ((int64_t)(v0 + v) * T + t) * H + n0 + c,
-                                                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                                          : 0.0f;
-#pragma unroll
-      for (int v = 0; v < 8; ++v) s += some[v];
-    }
-    y[(int64_t)t * H + n0 + c] = s;
+    for (int u = 1; u < 8; ++u) v += part[u][r];
+    y[n0 + r] = v;
   }
 }
 
@@ -404,63 +438,54 @@ hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, cons
   return hipGetLastError();
 }
 
-// How the two kernels of a call are laid out.  xp: token pieces (two tokens each) of the first; split:
-// workgroups that share a tile of the second; one: a single token, whose at most 16 experts fill the
-// waves of one workgroup per tile.
+// How a call's kernels are laid out.  xp: token pieces (two tokens each) of the first; one: a single token.
 struct MoePlan {
-  int xp, tile_rows, tiles, split;
-  bool one, small, join, few;
-  int64_t hidden_bytes, sum_bytes, counter_bytes;
+  int xp;
+  bool one, small, join;
+  int64_t hidden_bytes, product_bytes;
 };
 
 static MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   MoePlan m{};
   const int64_t P = T * k, most = P < E ? P : E;  // experts with pairs, at most
+  const bool dense = 2 * P > 5 * most || P > kFewPairs;
   m.small = P <= 64 && T <= 32;
   m.one = T == 1;
-  m.few = T <= 32;
-  m.xp = T <= 2 ? 1 : 2 * P <= 5 * most && P <= kFewPairs ? 2 : 4;
+  m.xp = T <= 2 ? 1 : dense ? 4 : 2;
   // tasks for about one wave a SIMD, or fewer: four waves share one
   m.join = m.small && most * ((I + 15) / 16) <= 4 * (int64_t)device_cu_count();
   if (m.join && m.xp > 2) m.xp = 2;
-  m.tile_rows = m.one ? 16 : 32;
-  m.tiles = (int)((H + m.tile_rows - 1) / m.tile_rows);
-  // the second kernel runs one workgroup a CU, each with a group for every wave
-  int64_t split = m.one ? 1 : (int64_t)device_cu_count() / m.tiles;
-  if (split > (most + 3) / 4) split = (most + 3) / 4;
-  m.split = (int)(split < 1 ? 1 : split > 32 ? 32 : split);
   auto pad = [](int64_t b) { return (b + 255) / 256 * 256; };
   m.hidden_bytes = pad(3 * P * I * 2);
-  m.sum_bytes = m.split > 1 ? pad((int64_t)m.split * T * H * 4) : 0;
-  m.counter_bytes = m.split > 1 ? pad((int64_t)m.tiles * 4) : 0;
+  m.product_bytes = m.one ? 0 : pad(P * H * 4);
   return m;
 }
 
 size_t mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   const MoePlan m = moe_plan(T, k, E, H, I);
-  return (size_t)(m.hidden_bytes + m.sum_bytes + m.counter_bytes);
+  return (size_t)(m.hidden_bytes + m.product_bytes);
 }
 
 namespace {
 
+// As many workgroups as run at a time, or as tasks there can be
 template <int XP, bool JOIN, bool SMALL>
-void gate_up_as(const MoeArgs& a, const MoePlan& m, uint16_t* h, uint32_t* counters, hipStream_t stream) {
-  // at most as many workgroups as run at a time, two a CU, and as tasks there can be
-  const int64_t each = JOIN ? 1 : 4, tasks = ((int64_t)a.T * a.k * ((a.I + 15) / 16) + each - 1) / each;
-  const int64_t slots = (XP == 2 ? 3 : 2) * (int64_t)device_cu_count();
-  const auto kernel = a.H % (2 * kMxChunk) ? moe_gate_up_kernel<XP, JOIN, SMALL, true>
-                                           : moe_gate_up_kernel<XP, JOIN, SMALL, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(tasks < slots ? tasks : slots)), dim3(256), 0, stream, a.T, a.k, a.E, a.H, a.I,
-                     a.x, a.ids, a.gate_codes, a.gate_scales, a.up_codes, a.up_scales, h, counters,
-                     m.split > 1 ? m.tiles : 0);
+void gate_up_as(const MoeArgs& a, uint16_t* h, hipStream_t stream) {
+  constexpr int WAVES = JOIN ? 4 : XP == 4 ? 8 : 12;
+  const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16), slots = (JOIN ? 2 : 1) * (int64_t)device_cu_count();
+  const auto kernel = a.H % (2 * kMxChunk) ? moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, true>
+                                           : moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tasks < slots ? tasks : slots)), dim3(WAVES * 64), 0, stream, a.T, a.k, a.E,
+                     a.H, a.I, a.x, a.ids, a.gate_codes, a.gate_scales, a.up_codes, a.up_scales, h);
 }
 
-template <int R, int XP, int DEPTH, int WAVES, int TOKENS, bool SMALL>
-void down_as(const MoeArgs& a, const MoePlan& m, const uint16_t* h, float* sums, uint32_t* counters, hipStream_t stream) {
-  const auto kernel = a.I % (2 * kMxChunk) ? moe_down_kernel<R, XP, DEPTH, WAVES, TOKENS, SMALL, true>
-                                           : moe_down_kernel<R, XP, DEPTH, WAVES, TOKENS, SMALL, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)m.tiles, (unsigned)m.split), dim3(WAVES * 64), 0, stream, a.T, a.k, a.E, a.H,
-                     a.I, h, a.ids, a.weights, a.down_codes, a.down_scales, a.y, sums, counters);
+template <int R, int XP, int WAVES, int PAIRS>
+void down_as(const MoeArgs& a, const uint16_t* h, float* products, hipStream_t stream) {
+  const int64_t tasks = (int64_t)a.T * a.k * ((a.H + 16 * R - 1) / (16 * R)), slots = device_cu_count();
+  const auto kernel = a.I % (2 * kMxChunk) ? moe_down_kernel<R, XP, WAVES, PAIRS, true>
+                                           : moe_down_kernel<R, XP, WAVES, PAIRS, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tasks < slots ? tasks : slots)), dim3(WAVES * 64), 0, stream, a.T, a.k, a.E,
+                     a.H, a.I, h, a.ids, a.down_codes, a.down_scales, products);
 }
 
 }  // namespace
@@ -469,20 +494,27 @@ hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream) {
   const MoePlan m = moe_plan(a.T, a.k, a.E, a.H, a.I);
   uint8_t* w = static_cast<uint8_t*>(a.workspace);
   uint16_t* h = reinterpret_cast<uint16_t*>(w);
-  float* sums = reinterpret_cast<float*>(w + m.hidden_bytes);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(w + m.hidden_bytes + m.sum_bytes);
+  float* products = reinterpret_cast<float*>(w + m.hidden_bytes);
   if (m.join) {
-    if (m.xp == 1) gate_up_as<1, true, true>(a, m, h, counters, stream);
-    else gate_up_as<2, true, true>(a, m, h, counters, stream);
-  } else if (m.xp == 1) gate_up_as<1, false, true>(a, m, h, counters, stream);
-  else if (m.xp == 2) m.small ? gate_up_as<2, false, true>(a, m, h, counters, stream) : gate_up_as<2, false, false>(a, m, h, counters, stream);
-  else m.small ? gate_up_as<4, false, true>(a, m, h, counters, stream) : gate_up_as<4, false, false>(a, m, h, counters, stream);
-  const hipError_t e = hipGetLastError();
+    if (m.xp == 1) gate_up_as<1, true, true>(a, h, stream);
+    else gate_up_as<2, true, true>(a, h, stream);
+  } else if (m.xp == 1) gate_up_as<1, false, true>(a, h, stream);
+  else if (m.xp == 2) m.small ? gate_up_as<2, false, true>(a, h, stream) : gate_up_as<2, false, false>(a, h, stream);
+  else m.small ? gate_up_as<4, false, true>(a, h, stream) : gate_up_as<4, false, false>(a, h, stream);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (m.one) down_as<1, 2, 4, 8, 1, true>(a, m, h, sums, counters, stream);
-  else if (m.small) down_as<2, 4, 2, 6, 32, true>(a, m, h, sums, counters, stream);
-  else if (m.few) down_as<2, 4, 2, 6, 32, false>(a, m, h, sums, counters, stream);
-  else down_as<2, 6, 2, 4, QL_MOE_MAX_TOKENS, false>(a, m, h, sums, counters, stream);
+  if (m.one) {
+    const auto kernel = a.I % (2 * kMxChunk) ? moe_down_one_kernel<true> : moe_down_one_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.H / 16)), dim3(512), 0, stream, a.k, a.E, a.H, a.I, h, a.ids, a.weights,
+                       a.down_codes, a.down_scales, a.y);
+    return hipGetLastError();
+  }
+  if (m.small) down_as<2, 6, 7, 64>(a, h, products, stream);
+  else down_as<2, 6, 7, kMaxPairs>(a, h, products, stream);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.H / 4 + 255) / 256), (unsigned)a.T), dim3(256), 0, stream, a.T, a.k,
+                     a.E, a.H, a.ids, a.weights, products, a.y);
   return hipGetLastError();
 }
 

@@ -90,6 +90,10 @@ __device__ __forceinline__ void dma16_two_if(bool first, bool second, uint32_t l
                   "s"(__builtin_amdgcn_readfirstlane(first ? ~0u : 0u)),
                   "s"(__builtin_amdgcn_readfirstlane(second ? ~0u : 0u)) : "memory");
 }
+__device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform_ptr(base)) : "memory");
+}
 __device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* p) {  // p per lane
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
@@ -115,24 +119,28 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // pairs of chunks first, first + step, ... .  A pair (256 inputs) of a tile is 128 bytes a row, whole
 // cache lines: read row by row straight into LDS (a lane order that the matrix instruction could take
 // from registers would touch 64 lines a load for 16 bytes each), as two pieces of eight rows, block b
-// of row r at column b ^ (r / 2 % 8); its scales are two dwords a row; a token is 512 bytes, granule g
-// (eight inputs) of token m at column g ^ m.  All operand reads are then free of bank conflicts.
+// of row r at column b ^ (r / 2 % 8); a token is 512 bytes, granule g (eight inputs) of token m at column
+// g ^ m.  Operand reads are then free of bank conflicts.  Scales are two dwords a row and pair: read for
+// kBand pairs at a time, as every read of a pair's alone would touch as many lines as its codes do.
 // DEPTH stages of the wave's own, no barrier.  The matrix instruction's lane (q, r) holds row r; token
 // 4q + i of row r comes out in acc[b][t][i].
+#ifndef QL_BAND
+#define QL_BAND 2
+#endif
 template <int NB, int R, int XP, int DEPTH>
 struct Skinny {
-  static constexpr int kTiles = NB * R, kScaleLoads = (kTiles + 1) / 2;
-  static constexpr int kScaleAt = kTiles * 2048, kXAt = kScaleAt + kScaleLoads * 256;
-  static constexpr int kStage = kXAt + XP * 1024;
-  static constexpr int kLds = DEPTH * kStage;  // per wave
-  static constexpr int kLoads = kTiles * 2 + kScaleLoads + XP;
-  static_assert(DEPTH * kLoads < 64, "the load counter has six bits");
+  static constexpr int kTiles = NB * R, kBand = QL_BAND, kScaleLoads = kTiles * kBand / 2;
+  static constexpr int kXAt = kTiles * 2048, kStage = kXAt + XP * 1024, kScales = kScaleLoads * 256;
+  static constexpr int kLds = DEPTH * (kStage + kScales);  // per wave: stages, then bands of scales
+  static constexpr int kLoads = kTiles * 2 + XP;
+  static_assert(DEPTH * (kLoads + kScaleLoads) < 64, "the load counter has six bits");
   static_assert(XP == 1 || XP % 2 == 0, "");
 
   const uint8_t* codes[NB];           // each 1024 below its matrix
+  const uint8_t* scales[NB];
   const uint8_t* x = nullptr;         // 1024 below the tokens (XP > 1)
   uint32_t code_off[2 * R];           // the lane's row and block of each piece (the first of two + 1024)
-  const uint8_t* scales[kScaleLoads];  // the lane's row and dword: lanes 0..31 an even tile, 32..63 the next
+  uint32_t scale_off[R * kBand / 2];  // the lane's row of each piece
   uint32_t x_off[XP];                 // the lane's token and granule (the first of two + 1024)
   int pieces = XP;                    // of the tokens: those past it are not loaded
 
@@ -159,12 +167,12 @@ struct Skinny {
       for (int h = 0; h < 2; ++h)
         code_off[2 * t + h] = (uint32_t)row(t, 8 * h + (lane >> 3)) * row_bytes + block(h) * 16 + (h ? 0 : 1024);
 #pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-      const int a = 2 * i, b = 2 * i + 1 < kTiles ? 2 * i + 1 : a;  // tiles in order of (matrix, tile)
-      const uint8_t* base = lane < 32 ? s[a / R] : s[b / R];
-      const int at = lane < 32 ? row(a % R, (lane >> 1) & 15) : row(b % R, (lane >> 1) & 15);
-      scales[i] = base + (uint32_t)at * stride + (lane & 1) * 4;
-    }
+    for (int b = 0; b < NB; ++b) scales[b] = s[b];
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int i = 0; i < kBand / 2; ++i)
+        scale_off[t * kBand / 2 + i] = (uint32_t)row(t, (i * 64 + lane) / (2 * kBand)) * stride;
     x = (const uint8_t*)tokens - (XP > 1 ? 1024 : 0);
 #pragma unroll
     for (int i = 0; i < XP; ++i)
@@ -178,23 +186,19 @@ struct Skinny {
     if (!now) {
       dma_none<kLoads>(lds, x);
     } else if (!TAIL || 8 * p + 8 <= nblk) {  // uniform
-      send_as(lds, p, [](int) { return 0u; }, 0u, [](int) { return 0u; });
+      send_as(lds, p, [](int) { return 0u; }, [](int) { return 0u; });
     } else {
-      const int lane = threadIdx.x & 63, nchunk = (nblk + 3) / 4;
       send_as(lds, p, [&](int h) { return (uint32_t)max(0, 8 * p + block(h) - (nblk - 1)) * 16; },
-              (uint32_t)max(0, 2 * p + (lane & 1) - (nchunk - 1)) * 4,
               [&](int i) { return (uint32_t)max(0, 32 * p + gran(i) - (K / 8 - 1)) * 16; });
     }
   }
   template <class Back, class XBack>
-  __device__ __forceinline__ void send_as(uint32_t lds, int p, Back back, uint32_t sback, XBack xback) const {
+  __device__ __forceinline__ void send_as(uint32_t lds, int p, Back back, XBack xback) const {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int t = 0; t < R; ++t)
         dma16_two(lds + (b * R + t) * 2048, codes[b] + (int64_t)p * 128, code_off[2 * t] - back(0), code_off[2 * t + 1] - back(1));
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) dma4(lds + kScaleAt + i * 256, scales[i] + (int64_t)p * 8 - sback);
     if constexpr (XP == 1) dma16_if(true, lds + kXAt, x + (int64_t)p * 512, x_off[0] - xback(0));
 #pragma unroll
     for (int i = 0; i + 1 < XP; i += 2)
@@ -202,11 +206,21 @@ struct Skinny {
                    x_off[i + 1] - xback(i + 1));
   }
 
-  // Adds pair p, whose stage is at st, to acc; the stage is read when `reading` is called.  xrow: the LDS
-  // row (token slot) that the lane's operand row r comes from.
+  // Loads the scales of pairs p, p + step, ..., kBand of them; those past a row's end repeat its last dword.
+  __device__ __forceinline__ void send_scales(uint32_t lds, int K, int p, int step) const {
+    const int slot = threadIdx.x & (2 * kBand - 1);
+    const uint32_t at = min((uint32_t)(2 * (p + (slot >> 1) * step) + (slot & 1)) * 4, (uint32_t)mx4_scale_stride(K) - 4);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < R * kBand / 2; ++i) dma4(lds + (b * R * kBand / 2 + i) * 256, scales[b], scale_off[i] + at);
+  }
+
+  // Adds pair p, whose stage is at st and whose scales are number `slot` of the band at sc, to acc; both are
+  // read when `reading` is called.  xrow: the LDS row (token slot) that the lane's operand row r comes from.
   template <bool TAIL, class Read>
-  static __device__ __forceinline__ void multiply(f32x4_t (&acc)[NB][R], const uint8_t* st, int K, int p, int xrow,
-                                                  Read reading) {
+  static __device__ __forceinline__ void multiply(f32x4_t (&acc)[NB][R], const uint8_t* st, const uint8_t* sc, int slot,
+                                                  int K, int p, int xrow, Read reading) {
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15, nblk = K / kMxBlock;
     u32x4_t w[NB][R][2], a[2][4];
     u32x2_t s[NB][R];
@@ -215,7 +229,7 @@ struct Skinny {
 #pragma unroll
       for (int t = 0; t < R; ++t) {
         const uint8_t* tile = st + (b * R + t) * 2048;
-        s[b][t] = *reinterpret_cast<const u32x2_t*>(st + kScaleAt + (b * R + t) * 128 + r * 8);
+        s[b][t] = *reinterpret_cast<const u32x2_t*>(sc + ((b * R + t) * 16 + r) * (8 * kBand) + slot * 8);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           w[b][t][h] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
@@ -227,7 +241,7 @@ struct Skinny {
         a[h][j] = *reinterpret_cast<const u32x4_t*>(st + kXAt + xrow * 512 + (((16 * h + 4 * q + j) ^ (xrow & 15)) << 4));
     wait_lgkm();
     reading();
-uint32_t e[NB][R][2];  // scale bytes
+    uint32_t e[NB][R][2];  // scale bytes
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -270,27 +284,37 @@ uint32_t e[NB][R][2];  // scale bytes
                                       Done done) {
     const int npair = (K / kMxBlock + 7) / 8;
     const uint32_t lds = lds_offset(smem);
-    bool more = first < npair && next(*this);
-    int ahead = first;
+    bool more = first < npair && next(*this), band = false;  // band: the newest stage came with scales
+    int ahead = first, slot_ahead = 0, band_ahead = 0;
     auto produce = [&](int d) __attribute__((always_inline)) {
+      band = more && slot_ahead == 0;
+      if (band) send_scales(lds + DEPTH * kStage + band_ahead * kScales, K, ahead, step);
       send<TAIL>(more, lds + d * kStage, K, min(ahead, npair - 1));
       if (more) {
         ahead += step;
-        if (ahead >= npair) ahead = first, more = next(*this);
+        const bool over = ahead >= npair;
+        if (over) ahead = first, more = next(*this);
+        slot_ahead = over || slot_ahead + 1 == kBand ? 0 : slot_ahead + 1;
+        if (slot_ahead == 0) band_ahead = band_ahead + 1 == DEPTH ? 0 : band_ahead + 1;
       }
     };
     for (int d = 0; d < DEPTH; ++d) produce(d);
-    int d = 0;
+    int d = 0, at = 0;  // the stage and the band in use
     for (int job = 0; job < jobs; ++job) {
       f32x4_t acc[NB][R];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int t = 0; t < R; ++t) acc[b][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int p = first; p < npair; p += step) {
-        wait_vm<(DEPTH - 1) * kLoads>();
-        multiply<TAIL>(acc, smem + d * kStage, K, p, xrow, [&]() __attribute__((always_inline)) { produce(d); });
+      for (int p = first, slot = 0; p < npair; p += step) {
+        // all but the newest DEPTH - 1 stages (with DEPTH > 2 a little more than that)
+        if (DEPTH == 2 && band) wait_vm<(DEPTH - 1) * kLoads + kScaleLoads>();
+        else wait_vm<(DEPTH - 1) * kLoads>();
+        multiply<TAIL>(acc, smem + d * kStage, smem + DEPTH * kStage + at * kScales, slot, K, p, xrow,
+                       [&]() __attribute__((always_inline)) { produce(d); });
         d = d + 1 == DEPTH ? 0 : d + 1;
+        slot = slot + 1 == kBand || p + step >= npair ? 0 : slot + 1;
+        if (slot == 0) at = at + 1 == DEPTH ? 0 : at + 1;
       }
       done(acc);
     }
