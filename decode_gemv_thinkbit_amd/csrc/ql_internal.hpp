@@ -76,9 +76,9 @@ hipError_t launch_mx4_quantize(int64_t rows, int64_t K, int type, const void* W,
                                hipStream_t stream);
 hipError_t launch_mx4_dequant(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, bool bf16,
                               void* out, hipStream_t stream);
-// Decode GEMV: 16-row tiles and waves per workgroup, and parts of K (over 1: sums in a workspace)
+// Decode GEMV: 16-row tiles per workgroup, and parts of K (over 1: sums in a workspace)
 struct GemvPlan {
-  int tiles, waves, parts;
+  int tiles, parts;
 };
 GemvPlan mx4_stream_plan(double token_bytes, int N, int K);
 GemvPlan mx4_gemv_plan(int M, int N, int K);

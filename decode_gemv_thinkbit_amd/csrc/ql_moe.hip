@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, i
     const uint8_t* __restrict__ gs, const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
     uint16_t* __restrict__ h) {
   constexpr int G = 2 * XP, kPairs = SMALL ? 64 : XP == 2 ? kFewPairs : kMaxPairs;
-  using S = Skinny<2, 1, XP, 2>;
+  using S = Skinny<2, 1, XP>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
   __shared__ typename Groups<kPairs, G>::Storage plan;
   __shared__ f32x4_t part[JOIN ? 2 : 1][JOIN ? 4 : 1][2][64];
@@ -300,26 +300,27 @@ template <int XP>
 __device__ __forceinline__ int plane_row(int r) { return min(3 * (r >> 2) + min(r & 3, 2), 2 * XP - 1); }
 __device__ __forceinline__ float planes(const f32x4_t& v) { return (v[2] + v[1]) + v[0]; }
 
-// products[p][n] = down row n on h[p].  A task is R tiles of 16 rows for one group; every wave takes tasks of
-// its own.
+// products[s][p][n] = part s of down row n on h[p].  A task is R tiles of 16 rows for one group; every wave
+// takes tasks of its own, or `split` (which divides WAVES) waves each a part of a task's pairs of chunks.
 template <int R, int XP, int WAVES, int PAIRS, bool TAIL>
-__global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int E, int H, int I,
+__global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int E, int H, int I, int split,
     const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint8_t* __restrict__ dc,
     const uint8_t* __restrict__ ds, float* __restrict__ products) {
   constexpr int G = 2 * XP / 3;
   static_assert(G <= 4, "");
-  using S = Skinny<1, R, XP, 2>;
+  using S = Skinny<1, R, XP>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
   __shared__ typename Groups<PAIRS, G>::Storage plan;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
   const int P = T * k, tiles = (H + 16 * R - 1) / (16 * R);
   const int tasks = Groups<PAIRS, G>::find(P, E, k, ids, plan, smem) * tiles;
-  const int first = first_task(wave), step = WAVES * (int)gridDim.x;
+  const int first = first_task(wave / split), step = WAVES / split * (int)gridDim.x;
   const int mine = tasks > first ? (tasks - 1 - first) / step + 1 : 0;
+  products += (int64_t)(wave % split) * P * H;
   S job;
   int ahead = first, now = first;
   job.template run<TAIL>(
-      smem + wave * S::kLds, I, 0, 1, plane_row<XP>(r), mine,
+      smem + wave * S::kLds, I, wave % split, split, plane_row<XP>(r), mine,
       [&](S& j) {
         if (ahead >= tasks) return false;
         const Group gr(plan.group[ahead / tiles]);
@@ -346,74 +347,65 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int 
       });
 }
 
-// y[t][n] = sum_j weights[t][j] products[t * k + j][n], over the pairs with an expert, in order of j: four
+// y[t][n] = sum_s sum_j weights[t][j] products[s][t * k + j][n], over the pairs with an expert, in order: four
 // outputs a thread.
-__global__ void __launch_bounds__(256) moe_join_kernel(int T, int k, int E, int H, const int32_t* __restrict__ ids,
-                                                       const float* __restrict__ weights,
+__global__ void __launch_bounds__(256) moe_join_kernel(int T, int k, int E, int H, int split,
+                                                       const int32_t* __restrict__ ids, const float* __restrict__ weights,
                                                        const float* __restrict__ products, float* __restrict__ y) {
   const int t = blockIdx.y, n = 4 * (int)(blockIdx.x * 256 + threadIdx.x);
   if (n >= H) return;
   f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    f32x4_t v[8];
+  for (int s = 0; s < split; ++s, products += (int64_t)T * k * H)
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      f32x4_t v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)  // pairs without an expert hold nothing: read, for one round of loads, and left out
-      v[j] = *reinterpret_cast<const f32x4_t*>(products + ((int64_t)t * k + min(j0 + j, k - 1)) * H + n);
+      for (int j = 0; j < 8; ++j)  // pairs without an expert hold nothing: read, for one round of loads, and left out
+        v[j] = *reinterpret_cast<const f32x4_t*>(products + ((int64_t)t * k + min(j0 + j, k - 1)) * H + n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int p = t * k + min(j0 + j, k - 1), id = ids[p];
-      const float w = weights[p];
-      const bool is = j0 + j < k && id >= 0 && id < E;
+      for (int j = 0; j < 8; ++j) {
+        const int p = t * k + min(j0 + j, k - 1), id = ids[p];
+        const float w = weights[p];
+        const bool is = j0 + j < k && id >= 0 && id < E;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] += is ? w * v[j][i] : 0.0f;
+        for (int i = 0; i < 4; ++i) sum[i] += is ? w * v[j][i] : 0.0f;
+      }
     }
-  }
   *reinterpret_cast<f32x4_t*>(y + (int64_t)t * H + n) = sum;
 }
 
-// One token: its experts (at most 16) fill the waves of one workgroup per 16 rows, whose sums are joined in
-// wave order; no second pass.
+// One token: its experts (at most 16) fill the waves of one workgroup per 16 rows, `split` of them to an
+// expert, dealt its pairs of chunks in turn; their sums are joined in wave order.  No second pass.
 template <bool TAIL>
-__global__ void __launch_bounds__(512) moe_down_one_kernel(int k, int E, int H, int I, const uint16_t* __restrict__ h,
-    const int32_t* __restrict__ ids, const float* __restrict__ weights, const uint8_t* __restrict__ dc,
-    const uint8_t* __restrict__ ds, float* __restrict__ y) {
-  using S = Skinny<1, 1, 2, 4>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * S::kLds];
-  __shared__ float part[8][16];
+__global__ void __launch_bounds__(1024) moe_down_one_kernel(int k, int E, int H, int I, int split,
+    const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const float* __restrict__ weights,
+    const uint8_t* __restrict__ dc, const uint8_t* __restrict__ ds, float* __restrict__ y) {
+  using S = Skinny<1, 1, 2>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[16 * S::kLds];
+  __shared__ float part[16][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15;
-  const int n0 = blockIdx.x * 16;
-  const int id = lane < k ? ids[lane] : -1;
-  const float weight = lane < k ? weights[lane] : 0.0f;
-  uint64_t left = __ballot(id >= 0 && id < E);  // the pairs to load yet, then those to add yet
-  for (int i = 0; i < wave; ++i) left &= left - 1;
-  uint64_t open = left;
-  auto take = [](uint64_t& v) __attribute__((always_inline)) {  // the next pair of this wave
-    const int p = __builtin_ctzll(v);
-    for (int i = 0; i < 8; ++i) v &= v - 1;
-    return p;
-  };
+  const int n0 = blockIdx.x * 16, pair = wave / split;
+  const int id = pair < k ? ids[pair] : -1;
+  const bool is = id >= 0 && id < E;
   float sum = 0.0f;
+  bool once = is;
   S job;
   job.template run<TAIL>(
-      smem + wave * S::kLds, I, 0, 1, plane_row<2>(r), ((int)__popcll(left) + 7) / 8,
+      smem + wave * S::kLds, I, wave % split, split, plane_row<2>(r), is ? 1 : 0,
       [&](S& j) {
-        if (!left) return false;
-        const int p = take(left);
-        const int64_t row = (int64_t)__builtin_amdgcn_readlane(id, p) * H + n0;
+        if (!once) return false;
+        once = false;
+        const int64_t row = (int64_t)id * H + n0;
         const uint8_t* const c[1] = {dc + row * (I / 2)};
         const uint8_t* const s[1] = {ds + row * mx4_scale_stride(I)};
-        j.init(I, c, s, [](int, int i) { return i; }, h, [&](int m) { return min(m, 2) * k + p; });
+        j.init(I, c, s, [](int, int i) { return i; }, h, [&](int m) { return min(m, 2) * k + pair; });
         return true;
       },
-      [&](const f32x4_t(&acc)[1][1]) {
-        sum += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), take(open))) * planes(acc[0][0]);
-      });
+      [&](const f32x4_t(&acc)[1][1]) { sum = weights[pair] * planes(acc[0][0]); });
   if (lane < 16) part[wave][r] = sum;
   __syncthreads();
   if (threadIdx.x < 16) {
     float v = part[0][r];
-#pragma unroll
-    for (int u = 1; u < 8; ++u) v += part[u][r];
+    for (int u = 1; u < k * split; ++u) v += part[u][r];
     y[n0 + r] = v;
   }
 }
@@ -438,9 +430,12 @@ hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, cons
   return hipGetLastError();
 }
 
-// How a call's kernels are laid out.  xp: token pieces (two tokens each) of the first; one: a single token.
+// How a call's kernels are laid out.  xp: token pieces (two tokens each) of the first; split: waves that
+// share a task of the second, where tasks are few and long; one: a single token.
+constexpr int kDownWaves = 12;
+
 struct MoePlan {
-  int xp;
+  int xp, split;
   bool one, small, join;
   int64_t hidden_bytes, product_bytes;
 };
@@ -455,9 +450,13 @@ static MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   // tasks for about one wave a SIMD, or fewer: four waves share one
   m.join = m.small && most * ((I + 15) / 16) <= 4 * (int64_t)device_cu_count();
   if (m.join && m.xp > 2) m.xp = 2;
+  m.split = 1;
+  if (m.small)
+    for (int split : {2, 3, 4, 6, 12})
+      if (most * ((H + 31) / 32) * split <= kDownWaves * (int64_t)device_cu_count() && I >= 1024 * split) m.split = split;
   auto pad = [](int64_t b) { return (b + 255) / 256 * 256; };
   m.hidden_bytes = pad(3 * P * I * 2);
-  m.product_bytes = m.one ? 0 : pad(P * H * 4);
+  m.product_bytes = m.one ? 0 : pad(m.split * P * H * 4);
   return m;
 }
 
@@ -471,8 +470,8 @@ namespace {
 // As many workgroups as run at a time, or as tasks there can be
 template <int XP, bool JOIN, bool SMALL>
 void gate_up_as(const MoeArgs& a, uint16_t* h, hipStream_t stream) {
-  constexpr int WAVES = JOIN ? 4 : XP == 4 ? 8 : 12;
-  const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16), slots = (JOIN ? 2 : 1) * (int64_t)device_cu_count();
+  constexpr int WAVES = JOIN ? 4 : 16;
+  const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16), slots = (JOIN ? XP == 1 ? 4 : 3 : 1) * (int64_t)device_cu_count();
   const auto kernel = a.H % (2 * kMxChunk) ? moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, true>
                                            : moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tasks < slots ? tasks : slots)), dim3(WAVES * 64), 0, stream, a.T, a.k, a.E,
@@ -480,12 +479,12 @@ void gate_up_as(const MoeArgs& a, uint16_t* h, hipStream_t stream) {
 }
 
 template <int R, int XP, int WAVES, int PAIRS>
-void down_as(const MoeArgs& a, const uint16_t* h, float* products, hipStream_t stream) {
+void down_as(const MoeArgs& a, int split, const uint16_t* h, float* products, hipStream_t stream) {
   const int64_t tasks = (int64_t)a.T * a.k * ((a.H + 16 * R - 1) / (16 * R)), slots = device_cu_count();
   const auto kernel = a.I % (2 * kMxChunk) ? moe_down_kernel<R, XP, WAVES, PAIRS, true>
                                            : moe_down_kernel<R, XP, WAVES, PAIRS, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tasks < slots ? tasks : slots)), dim3(WAVES * 64), 0, stream, a.T, a.k, a.E,
-                     a.H, a.I, h, a.ids, a.down_codes, a.down_scales, products);
+                     a.H, a.I, split, h, a.ids, a.down_codes, a.down_scales, products);
 }
 
 }  // namespace
@@ -504,17 +503,18 @@ hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (m.one) {
+    const int split = 16 / a.k;
     const auto kernel = a.I % (2 * kMxChunk) ? moe_down_one_kernel<true> : moe_down_one_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.H / 16)), dim3(512), 0, stream, a.k, a.E, a.H, a.I, h, a.ids, a.weights,
-                       a.down_codes, a.down_scales, a.y);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.H / 16)), dim3((unsigned)(a.k * split * 64)), 0, stream, a.k, a.E, a.H,
+                       a.I, split, h, a.ids, a.weights, a.down_codes, a.down_scales, a.y);
     return hipGetLastError();
   }
-  if (m.small) down_as<2, 6, 7, 64>(a, h, products, stream);
-  else down_as<2, 6, 7, kMaxPairs>(a, h, products, stream);
+  if (m.small) down_as<2, 6, kDownWaves, 64>(a, m.split, h, products, stream);
+  else down_as<2, 6, kDownWaves, kMaxPairs>(a, m.split, h, products, stream);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.H / 4 + 255) / 256), (unsigned)a.T), dim3(256), 0, stream, a.T, a.k,
-                     a.E, a.H, a.ids, a.weights, products, a.y);
+                     a.E, a.H, m.split, a.ids, a.weights, products, a.y);
   return hipGetLastError();
 }
 

@@ -97,11 +97,15 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(int64_t groups, uint32
 // y[m][n] = sum_k W[n][k] x[m][k]: a workgroup owns R tiles of 16 rows and one of the gridDim.y parts
 // of the inputs, its waves take pairs of chunks in turn and their sums are joined through LDS in wave
 // order; parts (more than one) go to `out` = [part][M][N] for mx4_join_kernel.
-template <int R, int XP, int WAVES, bool TAIL>
-__global__ void __launch_bounds__(WAVES * 64) mx4_gemv_kernel(int M, int N, int K, const uint8_t* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales,
-                                                              const uint16_t* __restrict__ x, float* __restrict__ out) {
-  using S = Skinny<1, R, XP, 2>;
+constexpr int kGemvWaves = 8;
+
+template <int R, int XP, bool TAIL>
+__global__ void __launch_bounds__(kGemvWaves * 64) mx4_gemv_kernel(int M, int N, int K, const uint8_t* __restrict__ codes,
+                                                                   const uint8_t* __restrict__ scales,
+                                                                   const uint16_t* __restrict__ x,
+                                                                   float* __restrict__ out) {
+  constexpr int WAVES = kGemvWaves;
+  using S = Skinny<1, R, XP>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
   static_assert(S::kLds >= R * 1024, "the sums are joined in the same memory");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
@@ -129,22 +133,22 @@ __global__ void __launch_bounds__(WAVES * 64) mx4_gemv_kernel(int M, int N, int 
 #pragma unroll
   for (int t = 0; t < R; ++t) part[(wave * R + t) * 64 + lane] = acc[0][t];
   __syncthreads();
-  if (wave < R) {
-    f32x4_t v = part[wave * 64 + lane];
-    for (int u = 1; u < WAVES; ++u) v += part[(u * R + wave) * 64 + lane];
-    const int64_t n = n0 + 16 * wave + r;
-    out += (int64_t)blockIdx.y * M * N;
+  out += (int64_t)blockIdx.y * M * N;
+  for (int t = wave; t < R; t += WAVES) {
+    f32x4_t v = part[t * 64 + lane];
+    for (int u = 1; u < WAVES; ++u) v += part[(u * R + t) * 64 + lane];
+    const int64_t n = n0 + 16 * t + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (4 * q + i < M && n < N) out[(int64_t)(4 * q + i) * N + n] = v[i];
   }
 }
 
-template <int R, int XP, int WAVES>
+template <int R, int XP>
 hipError_t gemv_as(int M, int N, int K, const uint8_t* codes, const uint8_t* scales, const uint16_t* x, int parts,
                    float* out, hipStream_t stream) {
-  const auto kernel = K % (2 * kMxChunk) ? mx4_gemv_kernel<R, XP, WAVES, true> : mx4_gemv_kernel<R, XP, WAVES, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)parts), dim3(WAVES * 64), 0, stream,
+  const auto kernel = K % (2 * kMxChunk) ? mx4_gemv_kernel<R, XP, true> : mx4_gemv_kernel<R, XP, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)parts), dim3(kGemvWaves * 64), 0, stream,
                      M, N, K, codes, scales, x, out);
   return hipGetLastError();
 }
@@ -152,12 +156,9 @@ hipError_t gemv_as(int M, int N, int K, const uint8_t* codes, const uint8_t* sca
 template <int XP>
 hipError_t gemv_tokens(const GemvPlan& g, int M, int N, int K, const uint8_t* codes, const uint8_t* scales,
                        const uint16_t* x, float* out, hipStream_t stream) {
-  if (g.tiles == 4) return gemv_as<4, XP, 4>(M, N, K, codes, scales, x, g.parts, out, stream);
-  if (g.tiles == 2) return gemv_as<2, XP, 4>(M, N, K, codes, scales, x, g.parts, out, stream);
-  if constexpr (XP <= 2) {
-    if (g.waves == 8) return gemv_as<1, XP, 8>(M, N, K, codes, scales, x, g.parts, out, stream);
-  }
-  return gemv_as<1, XP, 4>(M, N, K, codes, scales, x, g.parts, out, stream);
+  if (g.tiles == 4) return gemv_as<4, XP>(M, N, K, codes, scales, x, g.parts, out, stream);
+  if (g.tiles == 2) return gemv_as<2, XP>(M, N, K, codes, scales, x, g.parts, out, stream);
+  return gemv_as<1, XP>(M, N, K, codes, scales, x, g.parts, out, stream);
 }
 
 // y = the sum of `parts` arrays of n floats, in order
@@ -206,18 +207,19 @@ hipError_t launch_mx4_join(int64_t n, int parts, const float* in, float* y, hipS
 // What a CU has to fetch decides: a workgroup reads 17/32 bytes of each weight of its 16 R rows and
 // token_bytes per input, the tokens over again for every workgroup.  Few rows leave CUs
 // idle, so the rows per workgroup and the parts of K are chosen together for the least bytes per CU;
-// a second launch to join parts costs about 2 us of the GPU and more of the host, 150 KB at the 35 KB/us
-// that a CU was seen to fetch.
+// a second launch to join parts costs about 5 us, 175 KB at the 35 KB/us that a CU was seen to fetch
+// whatever the number of its waves (5120 x 17408 at 16 tokens: 28 / 22 / 29 us with 1 / 2 / 4 tiles, 18.0 with
+// 4 tiles and three parts; 4096 x 14336 at 8: 12.2 with 1 tile, 14.3 with 4 and three parts).
 GemvPlan mx4_stream_plan(double token_bytes, int N, int K) {
   const int64_t cus = device_cu_count(), pairs = (K + 2 * kMxChunk - 1) / (2 * kMxChunk);
-  GemvPlan best{1, 4, 1};
+  GemvPlan best{1, 1};
   double least = 0.0;
   for (int tiles = 1; tiles <= 4; tiles *= 2)
     for (int parts = 1; parts <= 8 && (parts == 1 || pairs >= 8 * parts); ++parts) {
       const int64_t groups = ((int64_t)N + 16 * tiles - 1) / (16 * tiles) * parts;
       const double rounds = (double)((groups + cus - 1) / cus);
-      const double cost = rounds * (8.5 * tiles + token_bytes) * K / parts + (parts > 1 ? 150e3 : 0.0);
-      if (least == 0.0 || cost < least) least = cost, best = {tiles, groups <= cus ? 8 : 4, parts};
+      const double cost = rounds * (8.5 * tiles + token_bytes) * K / parts + (parts > 1 ? 175e3 : 0.0);
+      if (least == 0.0 || cost < least) least = cost, best = {tiles, parts};
     }
   return best;
 }

@@ -61,8 +61,12 @@ __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, bf16x8_t b, f32x4_t c) {
 // blocks: one between a write of m0 and the load, five between a vector instruction's write of a scalar
 // register (a lane read of an address) and a load that uses it.
 
-// base computed by scalar instructions (a test reads the assembly for it)
 __device__ __forceinline__ void dma16(uint32_t lds, const uint8_t* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform_ptr(base)) : "memory");
+}
+// The same for an address and a base that scalar instructions made (a test reads the assembly for it)
+__device__ __forceinline__ void dma16_scalar(uint32_t lds, const uint8_t* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
@@ -75,20 +79,11 @@ __device__ __forceinline__ void dma16_if(bool now, uint32_t lds, const uint8_t* 
                   "s"(__builtin_amdgcn_readfirstlane(now ? ~0u : 0u)) : "memory");
 }
 // Two pieces, to lds and lds + 1024, from base + 1024 + off0 and base + 1024 + off1 (an instruction's
-// offset moves both of its addresses); each only if asked for.
+// offset moves both of its addresses).
 __device__ __forceinline__ void dma16_two(uint32_t lds, const uint8_t* base, uint32_t off0_plus_1024, uint32_t off1) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
                "global_load_lds_dwordx4 %2, %3 offset:1024"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off0_plus_1024), "v"(off1), "s"(uniform_ptr(base)) : "memory");
-}
-__device__ __forceinline__ void dma16_two_if(bool first, bool second, uint32_t lds, const uint8_t* base,
-                                             uint32_t off0_plus_1024, uint32_t off1) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\ts_nop 1\n\t"
-               "global_load_lds_dwordx4 %1, %3\n\ts_mov_b32 exec_lo, %5\n\ts_mov_b32 exec_hi, %5\n\t"
-               "global_load_lds_dwordx4 %2, %3 offset:1024\n\ts_mov_b64 exec, -1"
-               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off0_plus_1024), "v"(off1), "s"(uniform_ptr(base)),
-                  "s"(__builtin_amdgcn_readfirstlane(first ? ~0u : 0u)),
-                  "s"(__builtin_amdgcn_readfirstlane(second ? ~0u : 0u)) : "memory");
 }
 __device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2"
@@ -122,18 +117,15 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // of row r at column b ^ (r / 2 % 8); a token is 512 bytes, granule g (eight inputs) of token m at column
 // g ^ m.  Operand reads are then free of bank conflicts.  Scales are two dwords a row and pair: read for
 // kBand pairs at a time, as every read of a pair's alone would touch as many lines as its codes do.
-// DEPTH stages of the wave's own, no barrier.  The matrix instruction's lane (q, r) holds row r; token
+// One stage of the wave's own, no barrier: a pair is read into registers, the next one sent for, then the
+// products are made (two stages for half as many waves were as fast or slower).  The matrix instruction's lane (q, r) holds row r; token
 // 4q + i of row r comes out in acc[b][t][i].
-#ifndef QL_BAND
-#define QL_BAND 2
-#endif
-template <int NB, int R, int XP, int DEPTH>
+template <int NB, int R, int XP>
 struct Skinny {
-  static constexpr int kTiles = NB * R, kBand = QL_BAND, kScaleLoads = kTiles * kBand / 2;
-  static constexpr int kXAt = kTiles * 2048, kStage = kXAt + XP * 1024, kScales = kScaleLoads * 256;
-  static constexpr int kLds = DEPTH * (kStage + kScales);  // per wave: stages, then bands of scales
-  static constexpr int kLoads = kTiles * 2 + XP;
-  static_assert(DEPTH * (kLoads + kScaleLoads) < 64, "the load counter has six bits");
+  static constexpr int kTiles = NB * R, kBand = 2, kScaleLoads = kTiles * kBand / 2;
+  static constexpr int kXAt = kTiles * 2048, kScalesAt = kXAt + XP * 1024;
+  static constexpr int kLds = kScalesAt + kScaleLoads * 256;  // per wave
+  static_assert(kTiles * 2 + kScaleLoads + XP < 64, "the load counter has six bits");
   static_assert(XP == 1 || XP % 2 == 0, "");
 
   const uint8_t* codes[NB];           // each 1024 below its matrix
@@ -181,11 +173,9 @@ struct Skinny {
 
   // Loads pair p.  The last pair may end inside (TAIL): its blocks and granules past K repeat the last ones.
   template <bool TAIL>
-  __device__ __forceinline__ void send(bool now, uint32_t lds, int K, int p) const {
+  __device__ __forceinline__ void send(uint32_t lds, int K, int p) const {
     const int nblk = K / kMxBlock;
-    if (!now) {
-      dma_none<kLoads>(lds, x);
-    } else if (!TAIL || 8 * p + 8 <= nblk) {  // uniform
+    if (!TAIL || 8 * p + 8 <= nblk) {  // uniform
       send_as(lds, p, [](int) { return 0u; }, [](int) { return 0u; });
     } else {
       send_as(lds, p, [&](int h) { return (uint32_t)max(0, 8 * p + block(h) - (nblk - 1)) * 16; },
@@ -199,13 +189,14 @@ struct Skinny {
 #pragma unroll
       for (int t = 0; t < R; ++t)
         dma16_two(lds + (b * R + t) * 2048, codes[b] + (int64_t)p * 128, code_off[2 * t] - back(0), code_off[2 * t + 1] - back(1));
-    if constexpr (XP == 1) dma16_if(true, lds + kXAt, x + (int64_t)p * 512, x_off[0] - xback(0));
+    const uint8_t* xp = x + (int64_t)p * 512;
+    if constexpr (XP == 1) dma16(lds + kXAt, xp, x_off[0] - xback(0));
 #pragma unroll
-    for (int i = 0; i + 1 < XP; i += 2)
-      dma16_two_if(i < pieces, i + 1 < pieces, lds + kXAt + i * 1024, x + (int64_t)p * 512, x_off[i] - xback(i),
-                   x_off[i + 1] - xback(i + 1));
+    for (int i = 0; i + 1 < XP; i += 2) {
+      if (i + 1 < pieces) dma16_two(lds + kXAt + i * 1024, xp, x_off[i] - xback(i), x_off[i + 1] - xback(i + 1));
+      else if (i < pieces) dma16(lds + kXAt + i * 1024, xp, x_off[i] - xback(i));
+    }
   }
-
   // Loads the scales of pairs p, p + step, ..., kBand of them; those past a row's end repeat its last dword.
   __device__ __forceinline__ void send_scales(uint32_t lds, int K, int p, int step) const {
     const int slot = threadIdx.x & (2 * kBand - 1);
@@ -275,46 +266,36 @@ struct Skinny {
         }
   }
 
-  // The wave's whole work: a run of jobs of the same K, each over pairs first, first + step, ...; loads
-  // run DEPTH pairs ahead, into the next jobs too.  next(job) sets the loads up for the job after the last
-  // one it set up (false: no more); done(acc) takes a job's sums, in the same order, `jobs` times.
+  // The wave's whole work: a run of jobs of the same K, each over pairs first, first + step, ...; the next
+  // pair is under way while one is multiplied, into the next jobs too.  next(job) sets the loads up for the
+  // job after the last one it set up (false: no more); done(acc) takes a job's sums, in the same order, `jobs`
+  // times.
   //   smem: the wave's kLds bytes
   template <bool TAIL, class Next, class Done>
   __device__ __forceinline__ void run(const uint8_t* smem, int K, int first, int step, int xrow, int jobs, Next next,
                                       Done done) {
     const int npair = (K / kMxBlock + 7) / 8;
     const uint32_t lds = lds_offset(smem);
-    bool more = first < npair && next(*this), band = false;  // band: the newest stage came with scales
-    int ahead = first, slot_ahead = 0, band_ahead = 0;
-    auto produce = [&](int d) __attribute__((always_inline)) {
-      band = more && slot_ahead == 0;
-      if (band) send_scales(lds + DEPTH * kStage + band_ahead * kScales, K, ahead, step);
-      send<TAIL>(more, lds + d * kStage, K, min(ahead, npair - 1));
-      if (more) {
-        ahead += step;
-        const bool over = ahead >= npair;
-        if (over) ahead = first, more = next(*this);
-        slot_ahead = over || slot_ahead + 1 == kBand ? 0 : slot_ahead + 1;
-        if (slot_ahead == 0) band_ahead = band_ahead + 1 == DEPTH ? 0 : band_ahead + 1;
-      }
+    bool more = first < npair && next(*this);
+    int ahead = first, slot_ahead = 0;
+    auto produce = [&]() __attribute__((always_inline)) {
+      if (!more) return;
+      if (slot_ahead == 0) send_scales(lds + kScalesAt, K, ahead, step);
+      send<TAIL>(lds, K, ahead);
+      ahead += step;
+      slot_ahead = slot_ahead + 1 == kBand ? 0 : slot_ahead + 1;
+      if (ahead >= npair) ahead = first, slot_ahead = 0, more = next(*this);
     };
-    for (int d = 0; d < DEPTH; ++d) produce(d);
-    int d = 0, at = 0;  // the stage and the band in use
+    produce();
     for (int job = 0; job < jobs; ++job) {
       f32x4_t acc[NB][R];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int t = 0; t < R; ++t) acc[b][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int p = first, slot = 0; p < npair; p += step) {
-        // all but the newest DEPTH - 1 stages (with DEPTH > 2 a little more than that)
-        if (DEPTH == 2 && band) wait_vm<(DEPTH - 1) * kLoads + kScaleLoads>();
-        else wait_vm<(DEPTH - 1) * kLoads>();
-        multiply<TAIL>(acc, smem + d * kStage, smem + DEPTH * kStage + at * kScales, slot, K, p, xrow,
-                       [&]() __attribute__((always_inline)) { produce(d); });
-        d = d + 1 == DEPTH ? 0 : d + 1;
-        slot = slot + 1 == kBand || p + step >= npair ? 0 : slot + 1;
-        if (slot == 0) at = at + 1 == DEPTH ? 0 : at + 1;
+      for (int p = first, slot = 0; p < npair; p += step, slot = slot + 1 == kBand ? 0 : slot + 1) {
+        wait_vm<0>();
+        multiply<TAIL>(acc, smem, smem + kScalesAt, slot, K, p, xrow, produce);
       }
       done(acc);
     }

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) mx4_gemm_kernel(int M, int N,
   auto send_piece = [&](int p, int i) __attribute__((always_inline)) {
     const int pp = min(p, npair - 1);
     const uint32_t back = TAIL ? (uint32_t)max(0, 8 * pp + block - (nblk - 1)) * 16 : 0u;
-    dma16(lds0 + (p & 1) * S::kStage + (wave + S::kWaves * i) * 1024,
+    dma16_scalar(lds0 + (p & 1) * S::kStage + (wave + S::kWaves * i) * 1024,
           ((wave + S::kWaves * i) * 8 < S::kM ? xbase : wbase) + (int64_t)pp * 128, off[i] - back);
   };
   uint32_t scale_off[S::kScaleSends];

@@ -4,8 +4,8 @@ device code compiled for gfx950 keeps them (CPU only).
 - A load's scalar address is not written by a vector instruction (a lane read) in the five wait states
   before it, nor m0 by any instruction in the one before it.
 - Where a block narrows the active lanes, all of them are active again right behind its last load.
-- Every kernel with such loads waits for all of them before it ends: behind the last load, in the order of
-  the code, a wait for a count of 0 comes before the end.
+- Every kernel with such loads waits for all of them before it ends: every path of the code from a load to
+  the end passes a wait for a count of 0.
 """
 import concurrent.futures as cf
 import os
@@ -29,7 +29,7 @@ def device_asm(src):
 
 @pytest.fixture(scope="module")
 def kernels():
-    """{source: {kernel: [(instruction, operands)]}}"""
+    """{source: {kernel: [(instruction, operands)]}}; a label is an instruction without operands"""
     if not os.path.exists(qb.HIPCC):
         pytest.skip("hipcc not available")
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
@@ -38,7 +38,8 @@ def kernels():
     for src, text in texts.items():
         for name, body in re.findall(r"^(_ZN2ql\w*kernel\w*):(.*?)\.Lfunc_end", text, re.M | re.S):
             lines = [line.split(";")[0].strip() for line in body.split("\n")]
-            code = [line.replace(",", " ").split() for line in lines if line and not line.startswith(".")]
+            code = [line.replace(",", " ").split() for line in lines
+                    if line and (not line.startswith(".") or line.startswith(".LBB"))]
             out.setdefault(src, {})[name] = [(c[0], c[1:]) for c in code]
     return out
 
@@ -52,7 +53,7 @@ def scalars(operand):
 
 
 def states(op, operands):
-    return int(operands[0], 0) + 1 if op == "s_nop" else 1
+    return int(operands[0], 0) + 1 if op == "s_nop" else 0 if op.startswith(".LBB") else 1
 
 
 @pytest.mark.parametrize("src", SOURCES)
@@ -90,7 +91,20 @@ def test_all_lanes_return(kernels, src):
 @pytest.mark.parametrize("src", SOURCES)
 def test_loads_end_before_the_kernel(kernels, src):
     for name, code in kernels[src].items():
-        loads = [i for i, (op, _) in enumerate(code) if op.startswith("global_load_lds")]
-        if loads:
-            waits = [i for i, (op, r) in enumerate(code) if op == "s_waitcnt" and "vmcnt(0)" in r]
-            assert waits and waits[-1] > loads[-1], name
+        at_label = {op[:-1]: i for i, (op, _) in enumerate(code) if op.startswith(".LBB")}
+        seen = set()
+        todo = [i + 1 for i, (op, _) in enumerate(code) if op.startswith("global_load_lds")]
+        while todo:
+            i = todo.pop()
+            if i in seen:
+                continue
+            seen.add(i)
+            op, operands = code[i]
+            assert op != "s_endpgm", name
+            assert not op.startswith(("s_setpc", "s_swappc", "s_call")), name
+            if op == "s_waitcnt" and "vmcnt(0)" in operands:
+                continue
+            if op.startswith(("s_branch", "s_cbranch")):
+                todo.append(at_label[operands[0]])
+            if op != "s_branch":
+                todo.append(i + 1)
