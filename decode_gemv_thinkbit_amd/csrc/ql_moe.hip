@@ -43,6 +43,16 @@ __device__ __forceinline__ float wave_sum(float f) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
 }
 
+// the sum over the lanes up to this one
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
+  v += lanes_of<0x111, 0xF>(v);
+  v += lanes_of<0x112, 0xF>(v);
+  v += lanes_of<0x114, 0xF>(v);
+  v += lanes_of<0x118, 0xF>(v);
+  v += lanes_of<0x142, 0xA>(v);
+  return v + lanes_of<0x143, 0xC>(v);
+}
+
 template <int TYPE>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if constexpr (TYPE == QL_F32) return ((const float*)p)[i];
@@ -170,16 +180,12 @@ struct Groups {
         int slots = 0, groups = 0;  // running totals over the experts
         for (int e0 = 0; e0 < E; e0 += 64) {
           const int n = e0 + lane < E ? (int)sc.count[e0 + lane] : 0;
-          int both = n | ((n + G - 1) / G) << 16;
-          for (int d = 1; d < 64; d *= 2) {
-            const int left = __shfl_up(both, d);
-            if (lane >= d) both += left;
-          }
+          const int both = (int)wave_prefix((uint32_t)(n | ((n + G - 1) / G) << 16));
           if (e0 + lane < E) {
             const int before = both - (n | ((n + G - 1) / G) << 16);
             sc.start[e0 + lane] = (uint32_t)(slots + (before & 0xFFFF)) | (uint32_t)(groups + (before >> 16)) << 16;
           }
-          const int all = __shfl(both, 63);
+          const int all = __builtin_amdgcn_readlane(both, 63);
           slots += all & 0xFFFF, groups += all >> 16;
         }
         if (lane == 0) st.groups = groups;
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int 
       });
 }
 
-// y[t][n] = sum_s sum_j weights[t][j] products[s][t * k + j][n], over the pairs with an expert, in order: four
+// y[t][n] = sum_j weights[t][j] sum_s products[s][t * k + j][n], over the pairs with an expert, in order: four
 // outputs a thread.
 __global__ void __launch_bounds__(256) moe_join_kernel(int T, int k, int E, int H, int split,
                                                        const int32_t* __restrict__ ids, const float* __restrict__ weights,
@@ -355,21 +361,26 @@ __global__ void __launch_bounds__(256) moe_join_kernel(int T, int k, int E, int 
   const int t = blockIdx.y, n = 4 * (int)(blockIdx.x * 256 + threadIdx.x);
   if (n >= H) return;
   f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < split; ++s, products += (int64_t)T * k * H)
-    for (int j0 = 0; j0 < k; j0 += 8) {
-      f32x4_t v[8];
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    f32x4_t v[8];
+    const float* from = products + (int64_t)t * k * H + n;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // pairs without an expert hold nothing: read, for one round of loads, and left out
-        v[j] = *reinterpret_cast<const f32x4_t*>(products + ((int64_t)t * k + min(j0 + j, k - 1)) * H + n);
+    for (int j = 0; j < 8; ++j)  // pairs without an expert hold nothing: read, for one round of loads, and left out
+      v[j] = *reinterpret_cast<const f32x4_t*>(from + (int64_t)min(j0 + j, k - 1) * H);
+    for (int s = 1; s < split; ++s) {
+      from += (int64_t)T * k * H;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int p = t * k + min(j0 + j, k - 1), id = ids[p];
-        const float w = weights[p];
-        const bool is = j0 + j < k && id >= 0 && id < E;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += is ? w * v[j][i] : 0.0f;
-      }
+      for (int j = 0; j < 8; ++j) v[j] += *reinterpret_cast<const f32x4_t*>(from + (int64_t)min(j0 + j, k - 1) * H);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int p = t * k + min(j0 + j, k - 1), id = ids[p];
+      const float w = weights[p];
+      const bool is = j0 + j < k && id >= 0 && id < E;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += is ? w * v[j][i] : 0.0f;
+    }
+  }
   *reinterpret_cast<f32x4_t*>(y + (int64_t)t * H + n) = sum;
 }
 
@@ -400,13 +411,17 @@ __global__ void __launch_bounds__(1024) moe_down_one_kernel(int k, int E, int H,
         j.init(I, c, s, [](int, int i) { return i; }, h, [&](int m) { return min(m, 2) * k + pair; });
         return true;
       },
-      [&](const f32x4_t(&acc)[1][1]) { sum = weights[pair] * planes(acc[0][0]); });
+      [&](const f32x4_t(&acc)[1][1]) { sum = planes(acc[0][0]); });
   if (lane < 16) part[wave][r] = sum;
   __syncthreads();
   if (threadIdx.x < 16) {
-    float v = part[0][r];
-    for (int u = 1; u < k * split; ++u) v += part[u][r];
-    y[n0 + r] = v;
+    float all = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      float v = part[j * split][r];
+      for (int u = 1; u < split; ++u) v += part[j * split + u][r];
+      if (ids[j] >= 0 && ids[j] < E) all += weights[j] * v;
+    }
+    y[n0 + r] = all;
   }
 }
 

@@ -107,6 +107,55 @@ def test_moe(dev, T, E, k, H, I):
     check_moe(inputs(T, H, 5), torch.from_numpy(ids), torch.from_numpy(weights).float(), stacks(E, H, I, T, dev), dev)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 3, 1, 32, 96), (1, 8, 5, 64, 1056), (1, 16, 16, 96, 288), (1, 20, 9, 64, 1024),
+                                       (2, 8, 2, 64, 2080), (3, 4, 3, 96, 4128), (2, 3, 2, 64, 12320), (5, 3, 1, 32, 6176),
+                                       (8, 40, 4, 2080, 96), (64, 16, 4, 2048, 32), (20, 6, 4, 64, 2048)])
+def test_moe_shared_and_long_rows(dev, T, E, k, H, I):
+    """One token's experts among several waves, long rows of the down projection in parts, long inputs."""
+    g = torch.Generator().manual_seed(T + I)
+    ids, weights = ref.route(torch.randn(T, E, generator=g).double().numpy(), k, True)
+    check_moe(inputs(T, H, 6), torch.from_numpy(ids), torch.from_numpy(weights).float(), stacks(E, H, I, T, dev), dev)
+
+
+@pytest.mark.parametrize("ids", [[3, -1, 3, 9, 0], [-1, -1, -1, -1, -1], [6, 6, 6, 6, 6], [-1, 2, 7, -9, 1]])
+@pytest.mark.parametrize("I", [64, 1120])
+def test_moe_one_token_dropped_and_repeated(dev, ids, I):
+    ids = torch.tensor([ids], dtype=torch.int32)
+    weights = torch.tensor([[0.5, 0.25, -1.5, 2.0, 0.75]])
+    is_ = (ids >= 0) & (ids < 7)
+    experts, x = stacks(7, 96, I, 9, dev), inputs(1, 96, 2)
+    y = check_moe(x, ids, torch.where(is_, weights, 0.0), experts, dev)
+    loud = torch.where(is_, weights, float("nan"))
+    assert torch.equal(y, ql.mx4_moe(x.to(dev), ids.to(dev), loud.to(dev), *experts))
+
+
+@pytest.mark.parametrize("T,I", [(1, 1120), (2, 2080)])
+def test_moe_infinite_weight(dev, T, I):
+    """A weight multiplies an expert's whole sum, also where its rows are shared out: infinities keep signs."""
+    experts, x = stacks(4, 64, I, 2, dev), inputs(T, 64, 4).to(dev)
+    ids = torch.tensor([[2, 1]] * T, dtype=torch.int32, device=dev)
+    y = ql.mx4_moe(x, ids, torch.tensor([[1.0, 0.0]] * T, device=dev), *experts)
+    z = ql.mx4_moe(x, ids, torch.tensor([[INF, 0.0]] * T, device=dev), *experts)
+    assert (y != 0).all() and torch.equal(z, torch.where(y > 0, INF, -INF))
+
+
+def test_moe_beyond_four_gigabytes(dev):
+    """Experts whose codes lie beyond 32-bit offsets, and the same experts alone."""
+    E, H, I = 68, 8192, 16384
+    last = stacks(2, H, I, 3, dev)
+    big = [ql.Mx4Tensor(torch.zeros(E, *t.codes.shape[1:], dtype=torch.uint8, device=dev),
+                        torch.zeros(E, *t.scales.shape[1:], dtype=torch.uint8, device=dev)) for t in last]
+    for b, t in zip(big, last):
+        assert b.codes.numel() > 1 << 32
+        b.codes[-2:] = t.codes
+        b.scales[-2:] = t.scales
+    for T in (1, 2):  # as many pairs as experts at least: laid out alike, so equal
+        ids = torch.arange(T, device=dev, dtype=torch.int32).view(T, 1)
+        x, w = inputs(T, H, 5).to(dev), torch.ones(T, 1, device=dev)
+        y, z = ql.mx4_moe(x, ids + (E - 2), w, *big), ql.mx4_moe(x, ids, w, *last)
+        assert torch.equal(y, z) and (z != 0).any()
+
+
 def test_moe_all_tokens_one_expert(dev):
     T, E, H, I = 64, 9, 128, 96
     ids = torch.full((T, 1), 8, dtype=torch.int32)

@@ -211,3 +211,35 @@ def test_gemm_guarded_output(dev):
     ql.mx4_gemm(x, w, out=out)
     assert (buf[:64] == 7).all() and (buf[64 + M * N:] == 7).all()
     assert torch.equal(out, ql.mx4_gemm(x, w))
+
+
+# ---------------------------------------------------------------- beyond 32-bit offsets
+def test_products_beyond_four_gigabytes(dev):
+    """Rows whose codes lie beyond 4 GB, and outputs beyond 2^31 elements; exact sums (multiples of 0.5 far
+    below 2^24), so equal to the last rows alone."""
+    N, K, tail = 2200001, 4096, 130
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device=dev)
+    codes[-tail:] = torch.randint(0, 256, (tail, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.full((N, K // 32), 127, dtype=torch.uint8, device=dev)
+    w, last = ql.Mx4Tensor(codes, scales), ql.Mx4Tensor(codes[-tail:].clone(), scales[-tail:].clone())
+    for M in (1, 11):
+        x = torch.randint(-2, 3, (M, K), device=dev).bfloat16()
+        assert torch.equal(ql.mx4_gemv(x, w)[:, -tail:], ql.mx4_gemv(x, last))
+    for M in (40, 1000):
+        x = ql.mx4_quantize(torch.randint(-4, 5, (M, K), device=dev).float())
+        y = ql.mx4_gemm(x, w)
+        assert M < 1000 or y.numel() > 1 << 31
+        assert torch.equal(y[:, -tail:], ql.mx4_gemm(x, last)) and (y[:, :1000] == 0).all()
+        del y
+
+
+def test_quantize_beyond_two_billion(dev):
+    N, K, tail = 1050000, 2080, 37
+    W = torch.zeros(N, K, dtype=torch.bfloat16, device=dev)
+    assert W.numel() > 1 << 31
+    W[-tail:] = torch.randn(tail, K, device=dev)
+    t, last = ql.mx4_quantize(W), ql.mx4_quantize(W[-tail:].clone())
+    assert torch.equal(t.codes[-tail:], last.codes) and torch.equal(t.scales[-tail:], last.scales)
+    assert (t.codes[:5] == 0).all() and (t.scales[:5] == 0).all()
+    out = ql.mx4_dequant(t, out_bf16=True)
+    assert torch.equal(out[-tail:], ql.mx4_dequant(last, out_bf16=True))
