@@ -93,12 +93,6 @@ __device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* p) {  // p per
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
 }
-// n loads that read nothing, for the count
-template <int N>
-__device__ __forceinline__ void dma_none(uint32_t lds, const uint8_t* base) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) dma16_if(false, lds, base, 0u);
-}
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");

@@ -230,14 +230,16 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) mx4_gemm_kernel(int M, int N,
 // Up to 64 tokens: what bounds is the stream of W, so a workgroup owns R tiles of 16 rows (as the decode
 // GEMV, and with its split of K), MT tiles of 16 tokens ride along, and every wave runs whole pairs of
 // chunks through LDS stages of its own, tiles of W and of X laid out alike.
+constexpr int kSkinnyWaves = 8;
+
 template <int R, int MT, bool TAIL>
-__global__ void __launch_bounds__(256) mx4_gemm_skinny_kernel(int M, int N, int K, const uint8_t* __restrict__ xc,
+__global__ void __launch_bounds__(kSkinnyWaves * 64) mx4_gemm_skinny_kernel(int M, int N, int K, const uint8_t* __restrict__ xc,
     const uint8_t* __restrict__ xs, const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
     float* __restrict__ out) {
-  constexpr int kWaves = 4, kTiles = R + MT, kScaleLoads = (kTiles + 1) / 2;
-  constexpr int kScaleAt = kTiles * 2048, kStage = kScaleAt + kScaleLoads * 256, kLoads = 2 * kTiles + kScaleLoads;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kWaves * 2 * kStage];
-  static_assert(2 * kStage >= R * MT * 1024 && 2 * kLoads < 64, "");
+  constexpr int kWaves = kSkinnyWaves, kTiles = R + MT, kScaleLoads = (kTiles + 1) / 2;
+  constexpr int kScaleAt = kTiles * 2048, kStage = kScaleAt + kScaleLoads * 256;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kWaves * kStage];
+  static_assert(kStage >= R * MT * 1024 && 2 * kTiles + kScaleLoads < 64, "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
   const int nblk = K / kMxBlock, nchunk = (nblk + 3) / 4, npair = (nblk + 7) / 8;
   const uint32_t row_bytes = (uint32_t)K / 2, stride = (uint32_t)mx4_scale_stride(K);
@@ -264,15 +266,11 @@ __global__ void __launch_bounds__(256) mx4_gemm_skinny_kernel(int M, int N, int 
                           : (b < R ? wsb : xs) + (uint32_t)tile_row(b, row) * stride;
     scales[i] += (lane & 1) * 4;
   }
-  const uint8_t* mine = smem + wave * 2 * kStage;
+  const uint8_t* mine = smem + wave * kStage;
   const uint32_t lds = lds_offset(mine);
   const int step = kWaves * (int)gridDim.y, first = (int)blockIdx.y * kWaves + wave;
-  auto send = [&](int p, int d) __attribute__((always_inline)) {
-    const uint32_t at = lds + d * kStage;
-    if (p >= npair) {
-      dma_none<kLoads>(at, wc);
-      return;
-    }
+  auto send = [&](int p) __attribute__((always_inline)) {
+    if (p >= npair) return;
     const bool tail = TAIL && 8 * p + 8 > nblk;
     uint32_t back[2] = {0u, 0u}, sback = 0u;
     if (tail) {
@@ -282,32 +280,29 @@ __global__ void __launch_bounds__(256) mx4_gemm_skinny_kernel(int M, int N, int 
     }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
-      dma16_two(at + t * 2048, (t < R ? wb : xb) + (int64_t)p * 128, code_off[2 * t] - back[0], code_off[2 * t + 1] - back[1]);
+      dma16_two(lds + t * 2048, (t < R ? wb : xb) + (int64_t)p * 128, code_off[2 * t] - back[0], code_off[2 * t + 1] - back[1]);
 #pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) dma4(at + kScaleAt + i * 256, scales[i] + (int64_t)p * 8 - sback);
+    for (int i = 0; i < kScaleLoads; ++i) dma4(lds + kScaleAt + i * 256, scales[i] + (int64_t)p * 8 - sback);
   };
   f32x4_t acc[R][MT];
 #pragma unroll
   for (int t = 0; t < R; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  send(first, 0);
-  send(first + step, 1);
-  int d = 0;
-  for (int p = first; p < npair; p += step, d ^= 1) {
-    wait_vm<kLoads>();
+  send(first);
+  for (int p = first; p < npair; p += step) {
+    wait_vm<0>();
     u32x4_t c[kTiles][2];
     u32x2_t s[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const uint8_t* st = mine + d * kStage;
-      s[t] = *reinterpret_cast<const u32x2_t*>(st + kScaleAt + t * 128 + r * 8);
+      s[t] = *reinterpret_cast<const u32x2_t*>(mine + kScaleAt + t * 128 + r * 8);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        c[t][h] = *reinterpret_cast<const u32x4_t*>(st + t * 2048 + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
+        c[t][h] = *reinterpret_cast<const u32x4_t*>(mine + t * 2048 + r * 128 + (((4 * h + q) ^ (r >> 1)) << 4));
     }
     wait_lgkm();  // the stage is read: send into it
-    send(p + 2 * step, d);
+    send(p + step);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const bool in = !TAIL || 8 * p + 4 * h + q < nblk;  // blocks past K: zero codes of W, scales of 1
@@ -355,8 +350,8 @@ template <int R, int MT>
 hipError_t launch_skinny(int parts, int M, int N, int K, const uint8_t* xc, const uint8_t* xs, const uint8_t* wc,
                          const uint8_t* ws, float* out, hipStream_t stream) {
   const auto kernel = K % (2 * kMxChunk) ? mx4_gemm_skinny_kernel<R, MT, true> : mx4_gemm_skinny_kernel<R, MT, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)parts), dim3(256), 0, stream, M, N,
-                     K, xc, xs, wc, ws, out);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((N + 16 * R - 1) / (16 * R)), (unsigned)parts),
+                     dim3(kSkinnyWaves * 64), 0, stream, M, N, K, xc, xs, wc, ws, out);
   return hipGetLastError();
 }
 
