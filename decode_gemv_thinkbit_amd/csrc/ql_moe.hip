@@ -5,9 +5,11 @@ namespace ql {
 namespace {
 
 // ---------------------------------------------------------------- router
-// One wave per token.  Logits become unsigned keys of the same order (NaN and -inf become 0, which
-// is never taken), lane l holds experts l, 64 + l, ...; each of the k rounds takes the wave's largest
-// key and, among the lanes that hold it, the lowest expert.
+// One wave per token: latency bounds (16 tokens of 64 experts, 8 taken: 3.4 us, 4096 of 128: 5.4; an
+// empty launch takes 2), so everything stays in registers and crosses lanes in the vector unit.  Logits
+// become unsigned keys of the same order (NaN and -inf become 0, which is never taken), lane l holds
+// experts l, 64 + l, ...; each of the k rounds takes the wave's largest key and, among the lanes that
+// hold it, the lowest expert.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v);
   if ((b & 0x7FFFFFFFu) > 0x7F800000u || b == 0xFF800000u) return 0u;
@@ -115,8 +117,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(int64_t T, int E, int k,
 // to G, which share a read of its matrices.  Every workgroup finds them itself from the ids, into LDS: up
 // to 64 pairs in registers, every wave for itself; more by counting, with four barriers.
 constexpr int kMaxPairs = QL_MOE_MAX_TOKENS * QL_MOE_MAX_TOPK;
-static_assert(kMaxPairs <= 1024 && QL_MOE_MAX_TOKENS <= 64 && QL_MOE_MAX_EXPERTS <= 1024, "records of 10, 6 and 10 bits");
-constexpr int kFewPairs = 256;  // three workgroups of the gate and up kernel fit a CU's LDS, not two
+static_assert(kMaxPairs <= 1024 && QL_MOE_MAX_TOKENS <= 64 && QL_MOE_MAX_EXPERTS <= 1024, "records' bits");
 
 template <int PAIRS, int G>  // PAIRS: 64, or the most there may be
 struct Groups {
@@ -236,19 +237,22 @@ __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
 // h[p][i] = silu(g) * u with g, u the gate's and the up projection's row i on pair p's token.  A task is 16
 // rows of both for one group.  JOIN (few tasks): workgroups take tasks in turn, the inputs' pairs of
 // chunks dealt to the four waves and their sums joined in wave order; else every wave takes tasks of its
-// own.  Either way the next task's loads are under way while one ends.
+// own.  Either way the next task's loads are under way while one ends.  The stream of the experts' rows
+// bounds: 57 experts of 1536 x 4096 (380 MB) take 72 us, 5.3 TB/s; 87 of 768 x 2048 28 us, 5.2; of 736 x
+// 2080, whose rows are no whole cache lines, 33 us, 4.3.
 template <int XP, int WAVES, bool JOIN, bool SMALL, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, int E, int H, int I,
     const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint8_t* __restrict__ gc,
     const uint8_t* __restrict__ gs, const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
     uint16_t* __restrict__ h) {
-  constexpr int G = 2 * XP, kPairs = SMALL ? 64 : XP == 2 ? kFewPairs : kMaxPairs;
+  constexpr int G = 2 * XP, kPairs = SMALL ? 64 : kMaxPairs;
   using S = Skinny<2, 1, XP>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
   __shared__ typename Groups<kPairs, G>::Storage plan;
   __shared__ f32x4_t part[JOIN ? 2 : 1][JOIN ? 4 : 1][2][64];
   static_assert(!JOIN || WAVES == 4, "wave i finishes row i of every quarter");
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int P = T * k, tiles = (I + 15) / 16;
   const int tasks = Groups<kPairs, G>::find(P, E, k, ids, plan, smem) * tiles;
   const int first = JOIN ? (int)blockIdx.x : first_task(wave), step = (JOIN ? 1 : WAVES) * (int)gridDim.x;
@@ -308,6 +312,8 @@ __device__ __forceinline__ float planes(const f32x4_t& v) { return (v[2] + v[1])
 
 // products[s][p][n] = part s of down row n on h[p].  A task is R tiles of 16 rows for one group; every wave
 // takes tasks of its own, or `split` (which divides WAVES) waves each a part of a task's pairs of chunks.
+// What a CU fetches bounds: a row of W is 17/32 bytes an input, three planes of up to four pairs up to 24
+// (4096 x 1536 for 57 experts, 190 MB, 44 us; 4 tiles a task halve the planes' share).
 template <int R, int XP, int WAVES, int PAIRS, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int E, int H, int I, int split,
     const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint8_t* __restrict__ dc,
@@ -317,7 +323,8 @@ __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int 
   using S = Skinny<1, R, XP>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * S::kLds];
   __shared__ typename Groups<PAIRS, G>::Storage plan;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, r = lane & 15;
+  const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int P = T * k, tiles = (H + 16 * R - 1) / (16 * R);
   const int tasks = Groups<PAIRS, G>::find(P, E, k, ids, plan, smem) * tiles;
   const int first = first_task(wave / split), step = WAVES / split * (int)gridDim.x;
@@ -445,30 +452,42 @@ hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, cons
   return hipGetLastError();
 }
 
-// How a call's kernels are laid out.  xp: token pieces (two tokens each) of the first; split: waves that
-// share a task of the second, where tasks are few and long; one: a single token.
-constexpr int kDownWaves = 12;
+// How a call's kernels are laid out.
+//   one: a single token, whose experts fill the waves of a workgroup (8 of 64 experts of 1024 x 2048: 4.7 us
+//     against the 8.8 of products and their join).
+//   xp: token pieces (two tokens each) of the first kernel: two tokens need one; up to 16 else, as an expert
+//     with more pairs than a group holds is read again (128 experts of 1536 x 4096, 8 for 64 tokens: 176 us,
+//     with groups of 8 180, of 4 211; few pairs an expert cost nothing, as pieces without a token are not
+//     loaded).
+//   join: too few tasks for a wave on every SIMD: four waves share one (8 experts of 1024 x 2048: 6.8 us
+//     against 8.2; of 1536 x 4096 12.2 against 17.4; 15 of 1024 x 2048, about the bound, 9.1 both).
+//   wide: tasks of 64 rows in the second kernel where that leaves each wave three or more (those 128 experts:
+//     104 us against 118; 8 of 14336 x 4096, 2 for 64 tokens, on the other side, 207 against 178).
+//   split: waves that share a task of the second, where tasks are few and rows long (3 experts of 14336 x 4096:
+//     25 us against 49).
+constexpr int kDownWaves = 12, kWideWaves = 8;  // as their LDS and registers allow
 
 struct MoePlan {
   int xp, split;
-  bool one, small, join;
+  bool one, small, join, wide;
   int64_t hidden_bytes, product_bytes;
 };
 
 static MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   MoePlan m{};
   const int64_t P = T * k, most = P < E ? P : E;  // experts with pairs, at most
-  const bool dense = 2 * P > 5 * most || P > kFewPairs;
-  m.small = P <= 64 && T <= 32;
+  m.small = P <= 64;
   m.one = T == 1;
-  m.xp = T <= 2 ? 1 : dense ? 4 : 2;
-  // tasks for about one wave a SIMD, or fewer: four waves share one
+  m.xp = T <= 2 ? 1 : 8;
   m.join = m.small && most * ((I + 15) / 16) <= 4 * (int64_t)device_cu_count();
-  if (m.join && m.xp > 2) m.xp = 2;
+  if (m.join && m.xp > 1) m.xp = 2;
+  const int64_t groups = most > P / 4 ? most : P / 4;  // of the second kernel, about
+  m.wide = !m.small && groups * ((H + 63) / 64) >= 3 * kWideWaves * (int64_t)device_cu_count();
   m.split = 1;
   if (m.small)
     for (int split : {2, 3, 4, 6, 12})
-      if (most * ((H + 31) / 32) * split <= kDownWaves * (int64_t)device_cu_count() && I >= 1024 * split) m.split = split;
+      if (I >= 1024 * split && most * ((H + 31) / 32) * split <= kDownWaves * (int64_t)device_cu_count())
+        m.split = split;
   auto pad = [](int64_t b) { return (b + 255) / 256 * 256; };
   m.hidden_bytes = pad(3 * P * I * 2);
   m.product_bytes = m.one ? 0 : pad(m.split * P * H * 4);
@@ -485,8 +504,9 @@ namespace {
 // As many workgroups as run at a time, or as tasks there can be
 template <int XP, bool JOIN, bool SMALL>
 void gate_up_as(const MoeArgs& a, uint16_t* h, hipStream_t stream) {
-  constexpr int WAVES = JOIN ? 4 : 16;
-  const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16), slots = (JOIN ? XP == 1 ? 4 : 3 : 1) * (int64_t)device_cu_count();
+  constexpr int WAVES = JOIN ? 4 : XP == 1 ? 16 : 11;
+  const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16);
+  const int64_t slots = (JOIN ? XP == 1 ? 4 : 3 : 1) * (int64_t)device_cu_count();
   const auto kernel = a.H % (2 * kMxChunk) ? moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, true>
                                            : moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tasks < slots ? tasks : slots)), dim3(WAVES * 64), 0, stream, a.T, a.k, a.E,
@@ -513,8 +533,7 @@ hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream) {
     if (m.xp == 1) gate_up_as<1, true, true>(a, h, stream);
     else gate_up_as<2, true, true>(a, h, stream);
   } else if (m.xp == 1) gate_up_as<1, false, true>(a, h, stream);
-  else if (m.xp == 2) m.small ? gate_up_as<2, false, true>(a, h, stream) : gate_up_as<2, false, false>(a, h, stream);
-  else m.small ? gate_up_as<4, false, true>(a, h, stream) : gate_up_as<4, false, false>(a, h, stream);
+  else m.small ? gate_up_as<8, false, true>(a, h, stream) : gate_up_as<8, false, false>(a, h, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (m.one) {
@@ -525,11 +544,12 @@ hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream) {
     return hipGetLastError();
   }
   if (m.small) down_as<2, 6, kDownWaves, 64>(a, m.split, h, products, stream);
+  else if (m.wide) down_as<4, 6, kWideWaves, kMaxPairs>(a, m.split, h, products, stream);
   else down_as<2, 6, kDownWaves, kMaxPairs>(a, m.split, h, products, stream);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.H / 4 + 255) / 256), (unsigned)a.T), dim3(256), 0, stream, a.T, a.k,
-                     a.E, a.H, m.split, a.ids, a.weights, products, a.y);
+  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.H / 4 + 255) / 256), (unsigned)a.T), dim3(256), 0, stream, a.T,
+                     a.k, a.E, a.H, m.split, a.ids, a.weights, products, a.y);
   return hipGetLastError();
 }
 

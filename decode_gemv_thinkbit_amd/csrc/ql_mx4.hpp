@@ -32,8 +32,7 @@ typedef const __attribute__((address_space(1))) uint32_t* mx_gu32p;
 
 __host__ __device__ inline int64_t mx4_scale_stride(int64_t K) { return (K + kMxChunk - 1) / kMxChunk * 4; }
 
-// 16 bytes at p (global memory)
-__device__ __forceinline__ u32x4_t ld_b128(const void* p) { return *(gu32x4p)p; }
+// 16 or 4 bytes at p (global memory)
 __device__ __forceinline__ u32x4_t ld_b128_nt(const void* p) { return __builtin_nontemporal_load((gu32x4p)p); }
 __device__ __forceinline__ uint32_t ld_b32(const void* p) { return *(mx_gu32p)p; }
 
@@ -108,12 +107,12 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // pairs of chunks first, first + step, ... .  A pair (256 inputs) of a tile is 128 bytes a row, whole
 // cache lines: read row by row straight into LDS (a lane order that the matrix instruction could take
 // from registers would touch 64 lines a load for 16 bytes each), as two pieces of eight rows, block b
-// of row r at column b ^ (r / 2 % 8); a token is 512 bytes, granule g (eight inputs) of token m at column
-// g ^ m.  Operand reads are then free of bank conflicts.  Scales are two dwords a row and pair: read for
-// kBand pairs at a time, as every read of a pair's alone would touch as many lines as its codes do.
-// One stage of the wave's own, no barrier: a pair is read into registers, the next one sent for, then the
-// products are made (two stages for half as many waves were as fast or slower).  The matrix instruction's lane (q, r) holds row r; token
-// 4q + i of row r comes out in acc[b][t][i].
+// of row r at column b ^ (r / 2 % 8); a token is 512 bytes, granule g (eight inputs) of token m at
+// column g ^ m.  Operand reads are then free of bank conflicts.  Scales are two dwords a row and pair:
+// read for kBand pairs at a time, as every read of a pair's alone would touch as many lines as its
+// codes do. One stage of the wave's own, no barrier: a pair is read into registers, the next one sent
+// for, then the products are made (two stages for half as many waves were as fast or slower).  The
+// matrix instruction's lane (q, r) holds row r; token 4q + i of row r comes out in acc[b][t][i].
 template <int NB, int R, int XP>
 struct Skinny {
   static constexpr int kTiles = NB * R, kBand = 2, kScaleLoads = kTiles * kBand / 2;
