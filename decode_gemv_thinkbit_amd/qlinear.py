@@ -562,11 +562,11 @@ class Mx4Tensor:
             raise ValueError(f"codes and scales must be torch.uint8, got {c.dtype} and {s.dtype}")
         if not (c.is_contiguous() and s.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        *rows, half = c.shape
-        if len(rows) not in (1, 2) or half % 16 or not c.numel():
-            raise ValueError(f"codes must be [N, K/2] or [count, N, K/2] with K a multiple of 32, got {tuple(c.shape)}")
-        if [*s.shape] != [*rows, (half + 63) // 64 * 4]:
-            raise ValueError(f"scales of codes {tuple(c.shape)} must be [..., N, 4 * ceil(K/128)], got {tuple(s.shape)}")
+        *rows, half = shape = c.shape
+        if len(rows) not in (1, 2) or half % 16 or 0 in shape:
+            raise ValueError(f"codes must be [N, K/2] or [count, N, K/2] with K a multiple of 32, got {tuple(shape)}")
+        if s.shape != (*rows, (half + 63) // 64 * 4):
+            raise ValueError(f"scales of codes {tuple(shape)} must be [..., N, 4 * ceil(K/128)], got {tuple(s.shape)}")
         if c.device != s.device:
             raise ValueError("codes and scales must be on one device")
         object.__setattr__(self, "shape", (*rows, 2 * half))  # of the values
@@ -589,11 +589,12 @@ class Mx4Tensor:
 # takes 2.8 us of host time, more than the rest of a small call's checks together.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on_device(fn, device: torch.device, *args):
     """fn(*args) with `device` current."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -615,14 +616,14 @@ def _mx4(t: Mx4Tensor, dims: int, device: torch.device, name: str):
         raise ValueError(f"{name} must be an Mx4Tensor")
     if len(t.shape) != dims:
         raise ValueError(f"{name} must be {'a matrix' if dims == 2 else 'a stack of matrices'}, got {t.shape}")
-    if t.codes.device != device or device.type != "cuda":
+    if t.codes.device != device or not t.codes.is_cuda:
         raise ValueError(f"{name} must be on the device of the other operands, a CUDA (HIP) device")
     return t
 
 
 def _result(out: Optional[torch.Tensor], shape: tuple, dtype, device: torch.device, name: str = "out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     _dev(out, dtype, name)
     if out.shape != shape or out.device != device:
         raise ValueError(f"{name} must be {list(shape)} on {device}")
@@ -649,8 +650,8 @@ def mx4_quantize(W: torch.Tensor, out: Optional[Mx4Tensor] = None) -> Mx4Tensor:
         raise ValueError(f"W must be [N, K] or [count, N, K] with K a multiple of 32, got {tuple(W.shape)}")
     *rows, K = W.shape
     if out is None:
-        out = Mx4Tensor(torch.empty((*rows, K // 2), dtype=torch.uint8, device=W.device),
-                        torch.empty((*rows, 4 * ((K + 127) // 128)), dtype=torch.uint8, device=W.device))
+        out = Mx4Tensor(torch.empty(*rows, K // 2, dtype=torch.uint8, device=W.device),
+                        torch.empty(*rows, 4 * ((K + 127) // 128), dtype=torch.uint8, device=W.device))
     elif _mx4(out, W.dim(), W.device, "out").shape != W.shape:
         raise ValueError(f"out must be {tuple(W.shape)}")
     _launch("mx4_quantize", lib().qlinear_mx4_quantize, W.device, W.numel() // K, K, _DTYPES[W.dtype], W.data_ptr(),
@@ -673,15 +674,16 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
     _dev(x, torch.bfloat16, "x")
     if x.dim() == 1:
         x = x.view(1, -1)
-    _mx4(w, 2, x.device, "w")
+    device = x.device
+    _mx4(w, 2, device, "w")
     M, K = x.shape
-    N = w.N
-    if K != w.K:
-        raise ValueError(f"x has K={K}, weight has K={w.K}")
-    out = _result(out, (M, N), torch.float32, x.device)
-    need = _workspace_bytes("mx4_gemv", x.device, M, N, K)
-    workspace = _scratch(workspace, need, x.device) if need else None
-    _launch("mx4_gemv", lib().qlinear_mx4_gemv, x.device, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(),
+    N, inputs = w.shape
+    if K != inputs:
+        raise ValueError(f"x has K={K}, weight has K={inputs}")
+    out = _result(out, (M, N), torch.float32, device)
+    need = _workspace_bytes("mx4_gemv", device, M, N, K)
+    workspace = _scratch(workspace, need, device) if need else None
+    _launch("mx4_gemv", lib().qlinear_mx4_gemv, device, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(),
             x.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)
     return out
 
@@ -689,15 +691,18 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
 def mx4_gemm(x: Mx4Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [M, N] fp32 = x [M, K] times w [N, K] transposed, both MX4 (the scaled matrix instructions)."""
-    _mx4(x, 2, x.codes.device, "x")
-    _mx4(w, 2, x.codes.device, "w")
-    if x.K != w.K:
-        raise ValueError(f"x has K={x.K}, weight has K={w.K}")
-    M, N, K = x.N, w.N, w.K
-    out = _result(out, (M, N), torch.float32, x.codes.device)
-    need = _workspace_bytes("mx4_gemm", out.device, M, N, K)
-    workspace = _scratch(workspace, need, out.device) if need else None
-    _launch("mx4_gemm", lib().qlinear_mx4_gemm, out.device, M, N, K, x.codes.data_ptr(), x.scales.data_ptr(),
+    if not isinstance(x, Mx4Tensor):
+        raise ValueError("x must be an Mx4Tensor")
+    device = x.codes.device
+    _mx4(x, 2, device, "x")
+    _mx4(w, 2, device, "w")
+    (M, K), (N, inputs) = x.shape, w.shape
+    if K != inputs:
+        raise ValueError(f"x has K={K}, weight has K={inputs}")
+    out = _result(out, (M, N), torch.float32, device)
+    need = _workspace_bytes("mx4_gemm", device, M, N, K)
+    workspace = _scratch(workspace, need, device) if need else None
+    _launch("mx4_gemm", lib().qlinear_mx4_gemm, device, M, N, K, x.codes.data_ptr(), x.scales.data_ptr(),
             w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), workspace.data_ptr() if need else None, need)
     return out
 
@@ -716,9 +721,10 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, ids: Optio
     T, E = logits.shape
     if not 1 <= k <= min(E, MOE_MAX_TOPK):
         raise ValueError(f"k must be 1..{min(E, MOE_MAX_TOPK)}, got {k}")
-    ids = _result(ids, (T, k), torch.int32, logits.device, "ids")
-    weights = _result(weights, (T, k), torch.float32, logits.device, "weights")
-    _launch("moe_route", lib().qlinear_moe_route, logits.device, T, E, k, 1 if renormalize else 0,
+    device = logits.device
+    ids = _result(ids, (T, k), torch.int32, device, "ids")
+    weights = _result(weights, (T, k), torch.float32, device, "weights")
+    _launch("moe_route", lib().qlinear_moe_route, device, T, E, k, 1 if renormalize else 0,
             _DTYPES[logits.dtype], logits.data_ptr(), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
@@ -736,14 +742,14 @@ def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4
         raise ValueError("x must be [T, H], ids and weights [T, k]")
     T, H = x.shape
     k = ids.shape[1]
-    _mx4(gate, 3, x.device, "gate")
-    _mx4(up, 3, x.device, "up")
-    _mx4(down, 3, x.device, "down")
+    device = x.device
+    _mx4(gate, 3, device, "gate")
+    _mx4(up, 3, device, "up")
+    _mx4(down, 3, device, "down")
     E, I, inner = gate.shape
     if inner != H or up.shape != gate.shape or down.shape != (E, H, I):
         raise ValueError(f"x [T, {H}] needs gate and up [E, I, {H}] and down [E, {H}, I], got {gate.shape}, "
                          f"{up.shape}, {down.shape}")
-    device = x.device
     if ids.shape[0] != T or weights.shape != ids.shape or ids.device != device or weights.device != device:
         raise ValueError(f"ids and weights must be [{T}, k] on {device}")
     out = _result(out, (T, H), torch.float32, device)
