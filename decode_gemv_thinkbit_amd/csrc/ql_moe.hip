@@ -238,7 +238,7 @@ __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
 // rows of both for one group.  JOIN (few tasks): workgroups take tasks in turn, the inputs' pairs of
 // chunks dealt to the four waves and their sums joined in wave order; else every wave takes tasks of its
 // own.  Either way the next task's loads are under way while one ends.  The stream of the experts' rows
-// bounds: 57 experts of 1536 x 4096 (380 MB) take 72 us, 5.3 TB/s; 87 of 768 x 2048 28 us, 5.2; of 736 x
+// bounds: 57 experts of 1536 x 4096 (380 MB) take 72 us, 5.3 TB/s; 87 of 768 x 2048 27 us, 5.4; of 736 x
 // 2080, whose rows are no whole cache lines, 33 us, 4.3.
 template <int XP, int WAVES, bool JOIN, bool SMALL, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, int E, int H, int I,
@@ -460,7 +460,8 @@ hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, cons
 //     with groups of 8 180, of 4 211; few pairs an expert cost nothing, as pieces without a token are not
 //     loaded).
 //   join: too few tasks for a wave on every SIMD: four waves share one (8 experts of 1024 x 2048: 6.8 us
-//     against 8.2; of 1536 x 4096 12.2 against 17.4; 15 of 1024 x 2048, about the bound, 9.1 both).
+//     against 8.2; of 1536 x 4096 12.2 against 17.4; 15 of 1024 x 2048, about the bound, 9.1 both); its groups
+//     hold four pairs, so not where experts have more (2 of 4096 x 2048 for 64 tokens: 23.5 us, 12.0 without).
 //   wide: tasks of 64 rows in the second kernel where that leaves each wave three or more (those 128 experts:
 //     104 us against 118; 8 of 14336 x 4096, 2 for 64 tokens, on the other side, 207 against 178).
 //   split: waves that share a task of the second, where tasks are few and rows long (3 experts of 14336 x 4096:
@@ -479,7 +480,7 @@ static MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   m.small = P <= 64;
   m.one = T == 1;
   m.xp = T <= 2 ? 1 : 8;
-  m.join = m.small && most * ((I + 15) / 16) <= 4 * (int64_t)device_cu_count();
+  m.join = m.small && P <= 4 * most && most * ((I + 15) / 16) <= 4 * (int64_t)device_cu_count();
   if (m.join && m.xp > 1) m.xp = 2;
   const int64_t groups = most > P / 4 ? most : P / 4;  // of the second kernel, about
   m.wide = !m.small && groups * ((H + 63) / 64) >= 3 * kWideWaves * (int64_t)device_cu_count();

@@ -674,6 +674,8 @@ def mx4_gemv(x: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = None,
     _dev(x, torch.bfloat16, "x")
     if x.dim() == 1:
         x = x.view(1, -1)
+    elif x.dim() != 2:
+        raise ValueError("x must be [K] or [M, K]")
     device = x.device
     _mx4(w, 2, device, "w")
     M, K = x.shape

@@ -109,7 +109,8 @@ def test_moe(dev, T, E, k, H, I):
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 3, 1, 32, 96), (1, 8, 5, 64, 1056), (1, 16, 16, 96, 288), (1, 20, 9, 64, 1024),
                                        (2, 8, 2, 64, 2080), (3, 4, 3, 96, 4128), (2, 3, 2, 64, 12320), (5, 3, 1, 32, 6176),
-                                       (8, 40, 4, 2080, 96), (64, 16, 4, 2048, 32), (20, 6, 4, 64, 2048)])
+                                       (8, 40, 4, 2080, 96), (64, 16, 4, 2048, 32), (20, 6, 4, 64, 2048),
+                                       (64, 130, 16, 1568, 64), (64, 2, 1, 96, 1056)])
 def test_moe_shared_and_long_rows(dev, T, E, k, H, I):
     """One token's experts among several waves, long rows of the down projection in parts, long inputs."""
     g = torch.Generator().manual_seed(T + I)
