@@ -133,11 +133,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) mx4_gemm_kernel(int M, int N,
       b[t - 1] = *reinterpret_cast<const u32x4_t*>(st + (wn + 32 * (t - 1)) * 128 + (piece ^ (h * 32)));
     }
   };
-  // scale dword of chunk c for tile t (x tiles, then w tiles), shifted so that byte 2s is the lane's own
-  // block of the chunk's half step s
+  // scale dword of chunk c for tile t (x tiles, then w tiles); shifted by 8 half where it is used, so that
+  // nothing waits for a read: byte 2s is then the lane's own block of the chunk's half step s
   auto read_scale = [&](int c, int t) __attribute__((always_inline)) -> uint32_t {
     const uint8_t* st = sc + ((c >> 2) < full ? ((c >> 2) & 1) : 2) * S::kScales + (c & 3) * 4 + r * 16;
-    return *reinterpret_cast<const uint32_t*>(st + (t < MT ? wm + 32 * t : wn + 32 * (t - MT)) * 16) >> (8 * half);
+    return *reinterpret_cast<const uint32_t*>(st + (t < MT ? wm + 32 * t : wn + 32 * (t - MT)) * 16);
   };
   f32x16_t acc[MT][NT];
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) mx4_gemm_kernel(int M, int N,
 #pragma unroll
   for (int t = 0; t < kFrags; ++t) read(0, 0, t, A[0], B[0]);
 #pragma unroll
-  for (int t = 0; t < kFrags; ++t) (t < MT ? sa[t] : sb[t - MT]) = read_scale(0, t);
+  for (int t = 0; t < kFrags; ++t) (t < MT ? sa[t] : sb[t - MT]) = read_scale(0, t) >> (8 * half);
   // Each matrix instruction is a slot that also issues its share of the next half step's LDS reads, of
   // the next chunk's scales and of the pieces to send, so none of them holds up the matrix unit.
   int p = 0;
@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) mx4_gemm_kernel(int M, int N,
       }
       if (h & 1) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sa[i] = na[i];
+        for (int i = 0; i < MT; ++i) sa[i] = na[i] >> (8 * half);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) sb[j] = nb[j];
+        for (int j = 0; j < NT; ++j) sb[j] = nb[j] >> (8 * half);
       }
     }
   } while (++p < npair);
