@@ -238,8 +238,8 @@ __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
 // rows of both for one group.  JOIN (few tasks): workgroups take tasks in turn, the inputs' pairs of
 // chunks dealt to the four waves and their sums joined in wave order; else every wave takes tasks of its
 // own.  Either way the next task's loads are under way while one ends.  The stream of the experts' rows
-// bounds: 57 experts of 1536 x 4096 (380 MB) take 72 us, 5.3 TB/s; 87 of 768 x 2048 27 us, 5.4; of 736 x
-// 2080, whose rows are no whole cache lines, 33 us, 4.3.
+// bounds: 57 experts of 1536 x 4096 (380 MB) take 72 us, 5.3 TB/s; 87 of 768 x 2048 25 us, 5.8; of 736 x
+// 2080, whose rows are no whole cache lines, 30 us, 4.7.
 template <int XP, int WAVES, bool JOIN, bool SMALL, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, int E, int H, int I,
     const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint8_t* __restrict__ gc,
@@ -466,7 +466,12 @@ hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, cons
 //     104 us against 118; 8 of 14336 x 4096, 2 for 64 tokens, on the other side, 207 against 178).
 //   split: waves that share a task of the second, where tasks are few and rows long (3 experts of 14336 x 4096:
 //     25 us against 49).
-constexpr int kDownWaves = 12, kWideWaves = 8;  // as their LDS and registers allow
+// Waves of a workgroup, one to a CU: as many as LDS holds where tasks are few (42 experts of 1024 x 2048: gate and
+// up 16.9 us with 11 waves, 19.2 with 9, which take a second round); fewer where they are many, as fewer rows
+// under way keep the lines that two rows share in the L2 (88 of 736 x 2080: 33.0 us with 11, 30.4 with 9, 33.4
+// with 7; down 20.4 with 12, 19.1 with 10, 20.8 with 6).
+constexpr int kFewWaves = 12, kDownWaves = 10, kWideWaves = 8;
+
 
 struct MoePlan {
   int xp, split;
@@ -487,7 +492,7 @@ static MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   m.split = 1;
   if (m.small)
     for (int split : {2, 3, 4, 6, 12})
-      if (I >= 1024 * split && most * ((H + 31) / 32) * split <= kDownWaves * (int64_t)device_cu_count())
+      if (I >= 1024 * split && most * ((H + 31) / 32) * split <= kFewWaves * (int64_t)device_cu_count())
         m.split = split;
   auto pad = [](int64_t b) { return (b + 255) / 256 * 256; };
   m.hidden_bytes = pad(3 * P * I * 2);
@@ -505,7 +510,7 @@ namespace {
 // As many workgroups as run at a time, or as tasks there can be
 template <int XP, bool JOIN, bool SMALL>
 void gate_up_as(const MoeArgs& a, uint16_t* h, hipStream_t stream) {
-  constexpr int WAVES = JOIN ? 4 : XP == 1 ? 16 : 11;
+  constexpr int WAVES = JOIN ? 4 : XP == 1 ? 16 : SMALL ? 11 : 9;
   const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16);
   const int64_t slots = (JOIN ? XP == 1 ? 4 : 3 : 1) * (int64_t)device_cu_count();
   const auto kernel = a.H % (2 * kMxChunk) ? moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, true>
@@ -544,7 +549,7 @@ hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream) {
                        a.I, split, h, a.ids, a.weights, a.down_codes, a.down_scales, a.y);
     return hipGetLastError();
   }
-  if (m.small) down_as<2, 6, kDownWaves, 64>(a, m.split, h, products, stream);
+  if (m.small) down_as<2, 6, kFewWaves, 64>(a, m.split, h, products, stream);
   else if (m.wide) down_as<4, 6, kWideWaves, kMaxPairs>(a, m.split, h, products, stream);
   else down_as<2, 6, kDownWaves, kMaxPairs>(a, m.split, h, products, stream);
   e = hipGetLastError();
