@@ -275,3 +275,21 @@ def test_two_layers_in_graphs(dev):
         for got, want in zip(outs, eager):
             for a, b in zip(got, want):
                 assert torch.equal(a, b), step
+
+
+def test_layers_at_once_on_two_streams(dev):
+    """Two layers under way together, each on a stream of its own, give what they give alone."""
+    layers = [Layer(16, 16, 5, 512, 288, dev), Layer(2, 8, 2, 256, 2080, dev)]
+    xs = [inputs(16, 512, 8).to(dev), inputs(2, 256, 9).to(dev)]
+    want = [layer(x) for layer, x in zip(layers, xs)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(layers[i](xs[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for g in got[i]:
+            for a, b in zip(g, want[i]):
+                assert torch.equal(a, b)
