@@ -71,43 +71,6 @@ hipError_t launch_lb_pack(int64_t d_out, int64_t d_in, int64_t r, const int8_t* 
                           uint8_t* u_bits, uint8_t* v_bits, hipStream_t stream);
 hipError_t launch_lb_gemv(const ql_littlebit& w, const uint16_t* x, float* y, void* ws, hipStream_t stream);
 
-// microscaled 4-bit floats (ql_mx4.hip, ql_mx4_gemm.hip): row-major codes [rows][K/2] and scales
-hipError_t launch_mx4_quantize(int64_t rows, int64_t K, int type, const void* W, uint8_t* codes, uint8_t* scales,
-                               hipStream_t stream);
-hipError_t launch_mx4_dequant(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, bool bf16,
-                              void* out, hipStream_t stream);
-// Decode GEMV: 16-row tiles per workgroup, and parts of K (over 1: sums in a workspace)
-struct GemvPlan {
-  int tiles, parts;
-};
-GemvPlan mx4_stream_plan(double token_bytes, int N, int K);
-GemvPlan mx4_gemv_plan(int M, int N, int K);
-hipError_t launch_mx4_gemv(const GemvPlan& g, int M, int N, int K, const uint8_t* codes, const uint8_t* scales,
-                           const uint16_t* x, float* y, float* workspace, hipStream_t stream);
-hipError_t launch_mx4_join(int64_t n, int parts, const float* in, float* y, hipStream_t stream);
-struct GemmPlan {
-  int tiles, parts;  // the streaming kernel, as in GemvPlan (tiles > 0)
-  int tile;          // else which output tile
-};
-GemmPlan mx4_gemm_plan(int M, int N, int K);
-hipError_t launch_mx4_gemm(const GemmPlan& g, int M, int N, int K, const uint8_t* xc, const uint8_t* xs,
-                           const uint8_t* wc, const uint8_t* ws, float* y, float* workspace, hipStream_t stream);
-
-// mixture of experts (ql_moe.hip)
-hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, const void* logits, int32_t* ids,
-                            float* weights, hipStream_t stream);
-struct MoeArgs {
-  int32_t T, k, E, H, I;
-  const uint16_t* x;
-  const int32_t* ids;
-  const float* weights;
-  const uint8_t *gate_codes, *gate_scales, *up_codes, *up_scales, *down_codes, *down_scales;
-  float* y;
-  void* workspace;
-};
-size_t mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
-hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream);
-
 int device_cu_count();
 // read-bandwidth probe over `bytes` (a multiple of 1024) of device memory; out ^= XOR of the data
 hipError_t launch_read_probe(const void* buf, int64_t bytes, uint32_t* out, hipStream_t stream);
