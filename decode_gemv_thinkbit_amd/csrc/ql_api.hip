@@ -554,7 +554,8 @@ static ql_status check_topk(int64_t T, int64_t E, int64_t k) {
     return fail(QL_EINVAL, "1 <= E <= %d experts (E=%lld)", QL_MOE_MAX_EXPERTS, (long long)E);
   if (k < 1 || k > E || k > QL_MOE_MAX_TOPK)
     return fail(QL_EINVAL, "1 <= k <= min(E, %d) (k=%lld, E=%lld)", QL_MOE_MAX_TOPK, (long long)k, (long long)E);
-  if (T < 1 || T >= ((int64_t)1 << 26)) return fail(QL_EINVAL, "1 <= T < 2^26 tokens (T=%lld)", (long long)T);
+  // four tokens a workgroup of 256 threads: the grid stays below 2^32 threads
+  if (T < 1 || T > ((int64_t)1 << 26) - 4) return fail(QL_EINVAL, "1 <= T <= 2^26 - 4 tokens (T=%lld)", (long long)T);
   return QL_OK;
 }
 

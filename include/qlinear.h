@@ -448,7 +448,7 @@ ql_status qlinear_mx4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *x_cod
  * are never chosen: where fewer than k remain the id is -1 and the weight 0, so a row whose logits
  * are all -inf (a padded token) chooses nothing.  +inf takes all weight, shared by its equals.
  *   logits (dev) [T][E] of type dtype (ql_dtype); ids (dev) int32 [T][k]; weights (dev) fp32
- *   [T][k]; 1 <= k <= min(E, QL_MOE_MAX_TOPK), E <= QL_MOE_MAX_EXPERTS, 1 <= T < 2^26. */
+ *   [T][k]; 1 <= k <= min(E, QL_MOE_MAX_TOPK), E <= QL_MOE_MAX_EXPERTS, 1 <= T <= 2^26 - 4. */
 #define QL_MOE_MAX_EXPERTS 1024
 #define QL_MOE_MAX_TOPK 16
 #define QL_MOE_MAX_TOKENS 64
