@@ -224,10 +224,13 @@ __device__ __forceinline__ int first_task(int wave) {
   return wave * grid + (grid % 8 ? block : block % 8 * (grid / 8) + block / 8);
 }
 
-// The three bf16 planes of an fp32 value: hi + mid + lo == v to 24 bits (the second product then
-// runs on exact bf16 operands); of a value that is not finite only the first is kept.
+// The three bf16 planes of an fp32 value: hi + mid + lo == v from 2^-110 up (the second product then runs on
+// exact bf16 operands), below to half of 2^-133, the last plane's least step.  Where hi would round past the
+// largest bf16 (0x7F7F8000 and above) it is cut off instead, and the 16 bits left still fit the other two; of
+// a value that is not finite only the first is kept.
 __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
-  h[0] = f32_to_bf16_bits(v);
+  const uint32_t b = __float_as_uint(v);
+  h[0] = (b & 0x7FFFFFFFu) - 0x7F7F8000u < 0x8000u ? (uint16_t)(b >> 16) : f32_to_bf16_bits(v);
   const float r = v - bf16_bits_to_f32(h[0]);
   const bool fine = (h[0] & 0x7F80u) != 0x7F80u;
   h[1] = fine ? f32_to_bf16_bits(r) : 0;

@@ -460,7 +460,7 @@ ql_status qlinear_moe_route(int64_t T, int64_t E, int64_t k, int renormalize, in
  * silu(v) = v / (1 + exp(-v)).  Pairs whose id is outside 0..E-1 are left out (y[t] = 0 if all
  * are); an expert may appear twice in a row.  Only the experts that some token chose are read.
  * Products are exact and sums fp32 in a fixed order; the hidden values silu(gate) * up keep 24
- * significant bits.  Deterministic.
+ * significant bits, below 2^-110 those down to 2^-133.  Deterministic.
  *   x (dev) bf16 bits [T][H]; ids (dev) int32 [T][k], weights (dev) fp32 [T][k] (from
  *   qlinear_moe_route or any other router); gate, up: MX4 stacks of E matrices [I][H], down: of E
  *   matrices [H][I]; y (dev) fp32 [T][H]; workspace (dev, 16-byte aligned, contents need not be
