@@ -237,6 +237,16 @@ __device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
   h[2] = fine ? f32_to_bf16_bits(r - bf16_bits_to_f32(h[1])) : 0;
 }
 
+// silu(g) * u, silu(g) = g / (1 + exp(-g)).  Below -88, where exp(-g) overflows although the product need not
+// vanish, 1 + exp(-g) is exp(-g) to fp32, and exp(g) is taken in two halves, which stay in range.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  if (g < -88.0f) {
+    const float t = expf(0.5f * g);
+    return (g * t) * (t * u);
+  }
+  return g / (1.0f + expf(-g)) * u;
+}
+
 // h[p][i] = silu(g) * u with g, u the gate's and the up projection's row i on pair p's token.  A task is 16
 // rows of both for one group.  JOIN (few tasks): workgroups take tasks in turn, the inputs' pairs of
 // chunks dealt to the four waves and their sums joined in wave order; else every wave takes tasks of its
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, i
     const int n = now % tiles * 16 + r;
     if (slot < gr.count && n < I) {
       uint16_t hv[3];
-      split3(g / (1.0f + expf(-g)) * u, hv);
+      split3(swiglu(g, u), hv);
       const int64_t at = (int64_t)(plan.pair[gr.first + slot] & 1023) * I + n;
 #pragma unroll
       for (int z = 0; z < 3; ++z) h[z * (int64_t)P * I + at] = hv[z];

@@ -66,3 +66,20 @@ def test_small_values_keep_their_bits_down_to_the_least_bf16(dev, T):
     assert (h < 2.0 ** -110).any() and (h % 2.0 ** -133 != 0).any()
     got = hidden_through(x, gate, up, 40, T, dev) * 2.0 ** -40
     assert (np.abs(got - h) <= 2.0 ** -134).all() and np.array_equal(got[h >= 2.0 ** -110], h[h >= 2.0 ** -110])
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 64])
+def test_silu_where_its_exponential_overflows(dev, T):
+    """Gates below -88 with large up projections: exp(-g) is beyond fp32, silu(g) * u is not."""
+    x = [0.0] * 32
+    x[:4] = [80.0, 1.0, 8.0, 1.0]
+    more = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+    gate = matrix(32, 32, {(n, k): v for n in range(32) for k, v in ((0, -1.0), (1, -more[n % 8]), (2, -more[n // 4]))},
+                  [0] * 32, dev)
+    up = matrix(32, 32, {(n, 3): 1.0 if n % 3 else -1.0 for n in range(32)}, [100] * 32, dev)
+    g = np.array([-80.0 - more[n % 8] - 8 * more[n // 4] for n in range(32)])
+    h = g / (1 + np.exp(-g)) * np.where(np.arange(32) % 3, 1.0, -1.0) * 2.0 ** 100
+    assert (g < -89).sum() > 20 and (np.abs(h) > 2.0 ** -109).all()
+    # two exponentials within 2 steps each (4 half steps), their product twice that, four roundings, the third
+    # plane's last step, and the down projection's exact power of two
+    assert (np.abs(hidden_through(x, gate, up, 20, T, dev) * 2.0 ** -20 - h) <= 16 * 2.0 ** -24 * np.abs(h)).all()
