@@ -660,7 +660,9 @@ def mx4_quantize(W: torch.Tensor, out: Optional[Mx4Tensor] = None) -> Mx4Tensor:
 
 
 def mx4_dequant(t: Mx4Tensor, out_bf16: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The values of an MX4 tensor, fp32 or bf16 (exact in both)."""
+    """The values of an MX4 tensor, fp32 or bf16 (exact in both, but 4 * 2^127 and above are infinite)."""
+    if not isinstance(t, Mx4Tensor):
+        raise ValueError("t must be an Mx4Tensor")
     _mx4(t, len(t.shape), t.codes.device, "t")
     out = _result(out, t.shape, torch.bfloat16 if out_bf16 else torch.float32, t.codes.device)
     _launch("mx4_dequant", lib().qlinear_mx4_dequant, out.device, out.numel() // t.K, t.K, t.codes.data_ptr(),
