@@ -1,4 +1,7 @@
 // Mixture of experts for a few tokens: the router's choice, and the experts' products on MX4 weights.
+#include <algorithm>
+#include <cmath>
+
 #include "ql_mx4.hpp"
 
 namespace ql {
@@ -479,34 +482,41 @@ hipError_t launch_moe_route(int64_t T, int E, int k, bool renorm, int type, cons
 //     104 us against 118; 8 of 14336 x 4096, 2 for 64 tokens, on the other side, 207 against 178).
 //   split: waves that share a task of the second, where tasks are few and rows long (3 experts of 14336 x 4096:
 //     25 us against 49).
-// Waves of a workgroup, one to a CU: as many as LDS holds where tasks are few (42 experts of 1024 x 2048: gate and
-// up 16.9 us with 11 waves, 19.2 with 9, which take a second round); fewer where they are many, as fewer rows
-// under way keep the lines that two rows share in the L2 (88 of 736 x 2080: 33.0 us with 11, 30.4 with 9, 33.4
-// with 7; down 20.4 with 12, 19.1 with 10, 20.8 with 6).
-constexpr int kFewWaves = 12, kDownWaves = 10, kWideWaves = 8;
+//   gate_waves, down_waves: of a workgroup, one to a CU.  Fewer keep the lines that two rows share in the L2 and
+//     contend less; as many as LDS holds (11 and 12) are taken up to 64 pairs (10 tokens, 6 of 128 experts of 736 x
+//     2080: 40.5 us, with 9 and 10 42.4), and above where the tasks that T tokens with k of E experts each make on
+//     average need one round for two or two for three (9, 8 of 60 of 1024 x 2048, 2780 tasks: 41.1 against 43.4;
+//     24, 8 of 128 of 768 x 2048: 60.6 against 62.9; 20, 4 of 32 of 1408 x 2048: 41.8 against 45.4; with as many
+//     rounds 16, 8 of 60 of 1024 x 2048: 51.2 against 50.2, 32, 8 of 64 of 1536 x 4096: 155.5 against 151.1; five
+//     for six, 64, 8 of 128 of 1536 x 4096: 289 against 284).  In the second kernel only a single round is worth it
+//     (those 9 tokens: 1.1 us; 24, 6 of 128 of 736 x 2080, two rounds for three: 0.6 us the other way).
+constexpr int kGateWaves = 11, kGateFewer = 9, kDownWaves = 12, kDownFewer = 10, kWideWaves = 8;
 
-
-struct MoePlan {
-  int xp, split;
-  bool one, small, join, wide;
-  int64_t hidden_bytes, product_bytes;
-};
-
-static MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   MoePlan m{};
+  const int64_t cus = device_cu_count();
   const int64_t P = T * k, most = P < E ? P : E;  // experts with pairs, at most
   m.small = P <= 64;
   m.one = T == 1;
   m.xp = T <= 2 ? 1 : 8;
-  m.join = m.small && P <= 4 * most && most * ((I + 15) / 16) <= 4 * (int64_t)device_cu_count();
+  m.join = m.small && P <= 4 * most && most * ((I + 15) / 16) <= 4 * cus;
   if (m.join && m.xp > 1) m.xp = 2;
   const int64_t groups = most > P / 4 ? most : P / 4;  // of the second kernel, about
-  m.wide = !m.small && groups * ((H + 63) / 64) >= 3 * kWideWaves * (int64_t)device_cu_count();
+  m.wide = !m.small && groups * ((H + 63) / 64) >= 3 * kWideWaves * cus;
   m.split = 1;
   if (m.small)
     for (int split : {2, 3, 4, 6, 12})
-      if (I >= 1024 * split && most * ((H + 31) / 32) * split <= kFewWaves * (int64_t)device_cu_count())
-        m.split = split;
+      if (I >= 1024 * split && most * ((H + 31) / 32) * split <= kDownWaves * cus) m.split = split;
+  m.gate_waves = m.join ? 4 : m.xp == 1 ? 16 : kGateWaves;
+  m.down_waves = m.one ? (int)k * (16 / (int)k) : m.wide ? kWideWaves : kDownWaves;
+  if (!m.small) {
+    const double mean = (double)E * (1.0 - std::pow(1.0 - (double)k / (double)E, (double)T));  // experts with pairs
+    auto tasks = [&](int64_t group, int64_t tiles) { return (int64_t)(std::max(mean, (double)(P / group)) * tiles); };
+    auto rounds = [&](int64_t n, int waves) { return (n + waves * cus - 1) / (waves * cus); };
+    const int64_t gate = tasks(16, (I + 15) / 16), down = tasks(4, (H + 31) / 32);
+    if (rounds(gate, kGateWaves) > 2 || rounds(gate, kGateFewer) == rounds(gate, kGateWaves)) m.gate_waves = kGateFewer;
+    if (!m.wide && (down > kDownWaves * cus || down <= kDownFewer * cus)) m.down_waves = kDownFewer;
+  }
   auto pad = [](int64_t b) { return (b + 255) / 256 * 256; };
   m.hidden_bytes = pad(3 * P * I * 2);
   m.product_bytes = m.one ? 0 : pad(m.split * P * H * 4);
@@ -521,9 +531,8 @@ size_t mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64
 namespace {
 
 // As many workgroups as run at a time, or as tasks there can be
-template <int XP, bool JOIN, bool SMALL>
+template <int XP, int WAVES, bool JOIN, bool SMALL>
 void gate_up_as(const MoeArgs& a, uint16_t* h, hipStream_t stream) {
-  constexpr int WAVES = JOIN ? 4 : XP == 1 ? 16 : SMALL ? 11 : 9;
   const int64_t tasks = (int64_t)a.T * a.k * ((a.I + 15) / 16);
   const int64_t slots = (JOIN ? XP == 1 ? 4 : 3 : 1) * (int64_t)device_cu_count();
   const auto kernel = a.H % (2 * kMxChunk) ? moe_gate_up_kernel<XP, WAVES, JOIN, SMALL, true>
@@ -548,23 +557,24 @@ hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(a.workspace);
   uint16_t* h = reinterpret_cast<uint16_t*>(w);
   float* products = reinterpret_cast<float*>(w + m.hidden_bytes);
-  if (m.join) {
-    if (m.xp == 1) gate_up_as<1, true, true>(a, h, stream);
-    else gate_up_as<2, true, true>(a, h, stream);
-  } else if (m.xp == 1) gate_up_as<1, false, true>(a, h, stream);
-  else m.small ? gate_up_as<8, false, true>(a, h, stream) : gate_up_as<8, false, false>(a, h, stream);
+  if (m.join && m.xp == 1) gate_up_as<1, 4, true, true>(a, h, stream);
+  else if (m.join) gate_up_as<2, 4, true, true>(a, h, stream);
+  else if (m.xp == 1) gate_up_as<1, 16, false, true>(a, h, stream);
+  else if (m.small) gate_up_as<8, kGateWaves, false, true>(a, h, stream);
+  else if (m.gate_waves == kGateWaves) gate_up_as<8, kGateWaves, false, false>(a, h, stream);
+  else gate_up_as<8, kGateFewer, false, false>(a, h, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (m.one) {
-    const int split = 16 / a.k;
     const auto kernel = a.I % (2 * kMxChunk) ? moe_down_one_kernel<true> : moe_down_one_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.H / 16)), dim3((unsigned)(a.k * split * 64)), 0, stream, a.k, a.E, a.H,
-                       a.I, split, h, a.ids, a.weights, a.down_codes, a.down_scales, a.y);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.H / 16)), dim3((unsigned)(m.down_waves * 64)), 0, stream, a.k, a.E, a.H,
+                       a.I, m.down_waves / a.k, h, a.ids, a.weights, a.down_codes, a.down_scales, a.y);
     return hipGetLastError();
   }
-  if (m.small) down_as<2, 6, kFewWaves, 64>(a, m.split, h, products, stream);
+  if (m.small) down_as<2, 6, kDownWaves, 64>(a, m.split, h, products, stream);
   else if (m.wide) down_as<4, 6, kWideWaves, kMaxPairs>(a, m.split, h, products, stream);
-  else down_as<2, 6, kDownWaves, kMaxPairs>(a, m.split, h, products, stream);
+  else if (m.down_waves == kDownWaves) down_as<2, 6, kDownWaves, kMaxPairs>(a, m.split, h, products, stream);
+  else down_as<2, 6, kDownFewer, kMaxPairs>(a, m.split, h, products, stream);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.H / 4 + 255) / 256), (unsigned)a.T), dim3(256), 0, stream, a.T,

@@ -334,6 +334,13 @@ struct MoeArgs {
   float* y;
   void* workspace;
 };
+// How a call's kernels are laid out (the rules stand in ql_moe.hip; tests read this by its fields' order)
+struct MoePlan {
+  int xp, split, gate_waves, down_waves;
+  bool one, small, join, wide;
+  int64_t hidden_bytes, product_bytes;
+};
+MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 size_t mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 hipError_t launch_mx4_moe(const MoeArgs& a, hipStream_t stream);
 
