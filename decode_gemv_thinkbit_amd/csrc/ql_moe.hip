@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(256) moe_route_kernel(int64_t T, int E, int k,
 // ---------------------------------------------------------------- experts
 // A pair p = t * k + j is a token and one of its experts.  An expert's pairs, in order, make groups of up
 // to G, which share a read of its matrices.  Every workgroup finds them itself from the ids, into LDS: up
-// to 64 pairs in registers, every wave for itself; more by counting, with four barriers.
+// to 64 pairs in registers, every wave for itself; more by counting, with three barriers, the last of which gives
+// the scratch memory back.
 constexpr int kMaxPairs = QL_MOE_MAX_TOKENS * QL_MOE_MAX_TOPK;
 static_assert(kMaxPairs <= 1024 && QL_MOE_MAX_TOKENS <= 64 && QL_MOE_MAX_EXPERTS <= 1024, "records' bits");
 
@@ -254,8 +255,8 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // rows of both for one group.  JOIN (few tasks): workgroups take tasks in turn, the inputs' pairs of
 // chunks dealt to the four waves and their sums joined in wave order; else every wave takes tasks of its
 // own.  Either way the next task's loads are under way while one ends.  The stream of the experts' rows
-// bounds: 57 experts of 1536 x 4096 (380 MB) take 72 us, 5.3 TB/s; 87 of 768 x 2048 25 us, 5.8; of 736 x
-// 2080, whose rows are no whole cache lines, 30 us, 4.7.
+// bounds: traced, with weights from HBM, 57 experts of 1536 x 4096 (376 MB) take 74 us, 5.1 TB/s; 87 of 768 x 2048
+// (146 MB) 30 us, 4.9; 88 of 736 x 2080, whose rows are no whole cache lines, 37 us, 3.9.
 template <int XP, int WAVES, bool JOIN, bool SMALL, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_gate_up_kernel(int T, int k, int E, int H, int I,
     const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint8_t* __restrict__ gc,
@@ -329,7 +330,8 @@ __device__ __forceinline__ float planes(const f32x4_t& v) { return (v[2] + v[1])
 // products[s][p][n] = part s of down row n on h[p].  A task is R tiles of 16 rows for one group; every wave
 // takes tasks of its own, or `split` (which divides WAVES) waves each a part of a task's pairs of chunks.
 // What a CU fetches bounds: a row of W is 17/32 bytes an input, three planes of up to four pairs up to 24
-// (4096 x 1536 for 57 experts, 190 MB, 44 us; 4 tiles a task halve the planes' share).
+// (traced, from HBM, 4096 x 1536 for 57 experts, 190 MB, 44 us; 2048 x 768 for 87 19 us; 4 tiles a task halve the
+// planes' share).
 template <int R, int XP, int WAVES, int PAIRS, bool TAIL>
 __global__ void __launch_bounds__(WAVES * 64) moe_down_kernel(int T, int k, int E, int H, int I, int split,
     const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint8_t* __restrict__ dc,

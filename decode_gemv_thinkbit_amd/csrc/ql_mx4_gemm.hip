@@ -14,10 +14,11 @@ __device__ __forceinline__ f32x16_t mfma_mx4(u32x4_t a, u32x4_t b, f32x16_t c, u
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, SEL, (int)sa, SEL, (int)sb);
 }
 
-// WM x WN waves, (32 MT) x (32 NT) outputs each.  Bound by the matrix unit at the clock that it holds:
-// 4096 x 12288 x 4096 takes 114 us, 3.6 PFLOP/s; a loop of nothing but these instructions reaches 6.5 on
-// random operands (8.9 on zeros: the power, not the issue, limits), and storing y takes some 10 us more, at
-// the end of each workgroup.  512 tokens: 20 us.
+// WM x WN waves, (32 MT) x (32 NT) outputs each.  4096 x 12288 x K takes 26 us + 21 us per 1024 of K on random
+// operands: 114 us at K = 4096, 3.6 PFLOP/s.  The fixed part are the first loads and the stores of three tiles a
+// CU, while nothing else runs there (one workgroup fills its LDS).  The rest goes at 4.9 PFLOP/s, the matrix
+// unit busy in 65 % of the cycles, of which there are 1.7 10^9 a second (2.3 on zeros, 6.4 PFLOP/s: the power
+// sets the clock); a loop of nothing but these instructions reaches 6.5 (8.9 on zeros).  512 tokens: 20 us.
 //
 // A stage holds two chunks (256 inputs, a "pair") of the tile's rows: 128 bytes of codes a row, whole
 // cache lines, sent as 1 KB pieces of eight rows with 16 bytes a lane.  (64 bytes a row, one chunk a

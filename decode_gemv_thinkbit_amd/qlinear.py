@@ -552,7 +552,8 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # ql_dtype
 class Mx4Tensor:
     """A matrix [N, K], or a stack of matrices [count, N, K], of microscaled 4-bit floats: e2m1 codes,
     two per byte with the even input in the low nibble, and one scale byte s (2^(s - 127)) per 32
-    inputs, each row of scales padded to 4 * ceil(K / 128) bytes."""
+    inputs, each row of scales padded to 4 * ceil(K / 128) bytes (none where K is a multiple of 128; what
+    the padding holds is ignored)."""
     codes: torch.Tensor       # uint8 [..., N, K/2]
     scales: torch.Tensor      # uint8 [..., N, 4 * ceil(K/128)]
 

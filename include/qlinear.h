@@ -394,7 +394,8 @@ ql_status qlinear_lb_gemv(const ql_littlebit *w, const uint16_t *x, float *y, vo
  * microscaling format whose products gfx950's matrix unit computes directly:
  *   value = e2m1(code) * 2^(s - 127), code = sign (bit 3) and 0, 0.5, 1, 1.5, 2, 3, 4, 6 for
  *   bits 0..2 = 0..7; s = 255 makes the block's values NaN.
- * Storage is row-major, the order such checkpoints use, so no packing step is needed:
+ * Storage is row-major, the order such checkpoints use, so no packing step is needed (where K is no
+ * multiple of 128 a tensor of K/32 scales a row has to be copied into the padded rows below):
  *   codes  uint8 [N][K/2], the even input in the low nibble; K % 32 == 0;
  *   scales uint8 [N][qlinear_mx4_scale_stride(K)]: byte b of a row is the scale of inputs
  *          32b .. 32b+31; rows are padded to whole dwords, and what the padding holds is ignored.
@@ -464,7 +465,8 @@ ql_status qlinear_moe_route(int64_t T, int64_t E, int64_t k, int renormalize, in
  *   x (dev) bf16 bits [T][H]; ids (dev) int32 [T][k], weights (dev) fp32 [T][k] (from
  *   qlinear_moe_route or any other router); gate, up: MX4 stacks of E matrices [I][H], down: of E
  *   matrices [H][I]; y (dev) fp32 [T][H]; workspace (dev, 16-byte aligned, contents need not be
- *   zeroed) of qlinear_mx4_moe_workspace_bytes.  Calls that share a workspace must not overlap.
+ *   zeroed) of qlinear_mx4_moe_workspace_bytes on the current device.  Calls that share a workspace must
+ *   not overlap.
  * H and I are multiples of 32, at most 2^18. */
 typedef struct {
   int32_t E, H, I, k;
