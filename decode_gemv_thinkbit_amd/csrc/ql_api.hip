@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "ql_attn.hpp"
 #include "ql_internal.hpp"
 #include "ql_mx4.hpp"
 
@@ -593,6 +594,153 @@ ql_status qlinear_mx4_moe(const ql_mx4_experts* e, int64_t T, const uint16_t* x,
   const ql::MoeArgs a{(int32_t)T, e->k, e->E, e->H, e->I, x, e->ids, e->weights, e->gate_codes, e->gate_scales,
                       e->up_codes, e->up_scales, e->down_codes, e->down_scales, y, workspace};
   return hip_status(ql::launch_mx4_moe(a, stream), "mx4_moe launch");
+}
+
+// ---------------------------------------------------------------- rotary positions and attention
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // of 256 threads: a grid's side stays below 2^32
+
+static ql_status check_int32(std::initializer_list<const void*> ps) {
+  for (const void* p : ps) {
+    if (!p) return fail(QL_EINVAL, "null pointer argument");
+    if ((uintptr_t)p & 3u) return fail(QL_EINVAL, "pointer %p is not 4-byte aligned", p);
+  }
+  return QL_OK;
+}
+
+static ql_status check_heads(int64_t Hq, int64_t heads, int64_t dim) {
+  if (dim != 64 && dim != 128) return fail(QL_EINVAL, "heads of 64 or 128 dims (dim=%lld)", (long long)dim);
+  if (heads < 1 || heads > 4096 || Hq < 1 || Hq > 65536 || Hq % heads)
+    return fail(QL_EINVAL, "1..4096 kv heads and a multiple, at most 65536, of q heads (heads=%lld, Hq=%lld)",
+                (long long)heads, (long long)Hq);
+  return QL_OK;
+}
+
+static ql_status check_cache(const ql_kv_cache* c, int64_t Hq, ql::KvArgs* kv) {
+  if (!c) return fail(QL_EINVAL, "null cache");
+  QL_TRY(check_heads(Hq, c->heads, c->dim));
+  if (c->page < 16 || c->page > 4096 || (c->page & (c->page - 1)))
+    return fail(QL_EINVAL, "pages of 16..4096 tokens, a power of two (page=%d)", c->page);
+  if (c->pages < 1 || (int64_t)c->pages * c->page >= (int64_t)1 << 31)
+    return fail(QL_EINVAL, "1 <= pages, pages * page < 2^31 (pages=%d)", c->pages);
+  if (c->type != QL_BF16 && c->type != QL_E4M3) return fail(QL_EINVAL, "cache of type %d: bf16 or e4m3", c->type);
+  QL_TRY(check_ptrs({c->k, c->v}));
+  if (c->type == QL_E4M3) QL_TRY(check_int32({c->k_scale, c->v_scale}));
+  else if (c->k_scale || c->v_scale) return fail(QL_EINVAL, "a bf16 cache has no scales");
+  *kv = ql::KvArgs{(uint8_t*)c->k, (uint8_t*)c->v, c->k_scale, c->v_scale, c->pages, c->heads,
+                   __builtin_ctz((unsigned)c->page), c->dim, c->type == QL_E4M3};
+  return QL_OK;
+}
+
+static ql_status check_rows(int64_t T, int64_t heads, int64_t dim, int dtype, const void* p, int64_t stride) {
+  QL_TRY(check_ptrs({p}));
+  if (stride % (dtype == QL_F32 ? 4 : 8) || (T > 1 && stride < heads * dim) || stride < 0 || stride > (int64_t)1 << 32)
+    return fail(QL_EINVAL, "rows of %lld values need a stride of at least as many, a multiple of 16 bytes (stride=%lld)",
+                (long long)(heads * dim), (long long)stride);
+  return QL_OK;
+}
+
+ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                              const int32_t* slots, const ql_rope* rope, const float* q_norm, const float* k_norm,
+                              float eps, const ql_kv_cache* cache, uint16_t* out, hipStream_t stream) {
+  if (T < 1 || T > kMaxBlocks) return fail(QL_EINVAL, "1 <= T < 2^24 tokens (T=%lld)", (long long)T);
+  QL_TRY(check_dtype(dtype));
+  ql::RopeArgs a{};
+  QL_TRY(check_cache(cache, Hq, &a.kv));
+  if (!rope) return fail(QL_EINVAL, "null rope");
+  if (rope->dims < 2 || rope->dims > cache->dim || rope->dims % 2)
+    return fail(QL_EINVAL, "2..%d rotated dims, an even number (dims=%d)", cache->dim, rope->dims);
+  if (!std::isfinite(rope->factor)) return fail(QL_EINVAL, "rope's factor is not finite");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(QL_EINVAL, "eps must be finite, at least 0 (eps=%g)", (double)eps);
+  QL_TRY(check_rows(T, Hq, cache->dim, dtype, q, q_stride));
+  QL_TRY(check_rows(T, cache->heads, cache->dim, dtype, k, k_stride));
+  QL_TRY(check_rows(T, cache->heads, cache->dim, dtype, v, v_stride));
+  QL_TRY(check_int32({positions, slots, rope->freqs}));
+  if (q_norm) QL_TRY(check_int32({q_norm}));
+  if (k_norm) QL_TRY(check_int32({k_norm}));
+  QL_TRY(check_ptrs({out}));
+  a.q = q, a.k = k, a.v = v, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.positions = positions, a.slots = slots, a.freqs = rope->freqs, a.q_norm = q_norm, a.k_norm = k_norm, a.out = out;
+  a.factor = rope->factor, a.eps = eps, a.T = (int32_t)T, a.Hq = (int32_t)Hq, a.dims = rope->dims, a.dtype = dtype;
+  a.interleaved = rope->interleaved != 0;
+  return hip_status(ql::launch_rope_append(a, stream), "rope_append launch");
+}
+
+static ql_status check_attn_sizes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys) {
+  QL_TRY(check_heads(Hq, heads, dim));
+  if (B < 1 || B > kMaxBlocks) return fail(QL_EINVAL, "1 <= B < 2^24 sequences (B=%lld)", (long long)B);
+  if (keys < 1 || keys >= (int64_t)1 << 31)
+    return fail(QL_EINVAL, "a row of the table holds 1 .. 2^31 - 1 tokens (%lld)", (long long)keys);
+  return QL_OK;
+}
+
+static ql_status check_decode_sizes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys) {
+  QL_TRY(check_attn_sizes(B, Hq, heads, dim, keys));
+  if (B * Hq > kMaxBlocks / 2 || B * ((keys + 127) / 128) >= (int64_t)1 << 31)
+    return fail(QL_EINVAL, "too many sequences (B=%lld, Hq=%lld, keys=%lld)", (long long)B, (long long)Hq, (long long)keys);
+  return QL_OK;
+}
+
+static ql_status check_prompt_sizes(int64_t T, int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys) {
+  QL_TRY(check_attn_sizes(B, Hq, heads, dim, keys));
+  if (T < 1 || T > kMaxBlocks || T * Hq >= (int64_t)1 << 31)
+    return fail(QL_EINVAL, "1 <= T < 2^24 queries, T * Hq < 2^31 (T=%lld, Hq=%lld)", (long long)T, (long long)Hq);
+  if (ql::attn_prompt_blocks(T, B, Hq, heads, dim, keys) > kMaxBlocks)
+    return fail(QL_EINVAL, "too many queries and sequences (T=%lld, B=%lld, Hq=%lld)", (long long)T, (long long)B, (long long)Hq);
+  return QL_OK;
+}
+
+static ql_status check_attn(const ql_kv_cache* cache, int64_t B, int64_t Hq, const uint16_t* q, const int32_t* table,
+                            int64_t table_stride, int64_t max_pages, const int32_t* lens, float scale, uint16_t* out,
+                            ql::AttnArgs* a) {
+  QL_TRY(check_cache(cache, Hq, &a->kv));
+  if (max_pages < 1 || max_pages >= (int64_t)1 << 31 || (B > 1 && table_stride < max_pages))
+    return fail(QL_EINVAL, "a table of at least one page, rows no nearer than they are long (max_pages=%lld, stride=%lld)",
+                (long long)max_pages, (long long)table_stride);
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QL_EINVAL, "scale must be positive and finite (scale=%g)", (double)scale);
+  QL_TRY(check_ptrs({q, out}));
+  QL_TRY(check_int32({table, lens}));
+  a->q = q, a->table = table, a->lens = lens, a->table_stride = table_stride, a->out = out;
+  a->score_scale = scale * 1.4426950408889634f, a->B = (int32_t)B, a->Hq = (int32_t)Hq;
+  return QL_OK;
+}
+
+size_t qlinear_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys) {
+  return check_decode_sizes(B, Hq, heads, dim, keys) == QL_OK ? ql::attn_decode_workspace_bytes(B, Hq, heads, dim, keys) : 0;
+}
+
+ql_status qlinear_attn_decode(const ql_kv_cache* cache, int64_t B, int64_t Hq, const uint16_t* q,
+                              const int32_t* table, int64_t table_stride, int64_t max_pages, const int32_t* lens,
+                              float scale, uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  ql::AttnArgs a{};
+  QL_TRY(check_attn(cache, B, Hq, q, table, table_stride, max_pages, lens, scale, out, &a));
+  const int64_t keys = max_pages * cache->page;
+  QL_TRY(check_decode_sizes(B, Hq, cache->heads, cache->dim, keys));
+  const size_t need = ql::attn_decode_workspace_bytes(B, Hq, cache->heads, cache->dim, keys);
+  if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
+  if (need) QL_TRY(check_ptrs({workspace}));
+  a.ws = static_cast<float*>(workspace), a.keys = (int32_t)keys;
+  return hip_status(ql::launch_attn_decode(a, stream), "attn_decode launch");
+}
+
+size_t qlinear_attn_prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys) {
+  return check_prompt_sizes(T, B, Hq, heads, dim, keys) == QL_OK ? ql::attn_prompt_workspace_bytes(T, B, Hq, heads, dim, keys) : 0;
+}
+
+ql_status qlinear_attn_prompt(const ql_kv_cache* cache, int64_t T, int64_t B, int64_t Hq, const uint16_t* q,
+                              const int32_t* starts, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                              const int32_t* lens, float scale, uint16_t* out, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  ql::AttnArgs a{};
+  QL_TRY(check_attn(cache, B, Hq, q, table, table_stride, max_pages, lens, scale, out, &a));
+  QL_TRY(check_int32({starts}));
+  const int64_t keys = max_pages * cache->page;
+  QL_TRY(check_prompt_sizes(T, B, Hq, cache->heads, cache->dim, keys));
+  const size_t need = ql::attn_prompt_workspace_bytes(T, B, Hq, cache->heads, cache->dim, keys);
+  if (workspace_bytes < need) return fail(QL_EINVAL, "workspace too small (%zu < %zu)", workspace_bytes, need);
+  if (need) QL_TRY(check_ptrs({workspace}));
+  a.ws = static_cast<float*>(workspace), a.keys = (int32_t)keys, a.T = (int32_t)T, a.starts = starts;
+  return hip_status(ql::launch_attn_prompt(a, stream), "attn_prompt launch");
 }
 
 ql_status qlinear_read_probe(const void* buf, int64_t bytes, uint32_t* out, hipStream_t stream) {

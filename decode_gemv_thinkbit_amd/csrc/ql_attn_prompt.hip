@@ -1,0 +1,430 @@
+// Causal attention of packed prompts (or chunks of them) over the paged cache.
+//
+// Sequence b's queries are rows starts[b] .. starts[b + 1] - 1 (n of them), its last query the last of its
+// len = lens[b] cached tokens: query i sees the keys up to position len - n + i.  The G = Hq / Hkv heads of a
+// kv head see the same keys, so rows of a tile are (query, head) pairs, 128 of n * G: short chunks of many
+// heads fill a tile as long ones do.
+//
+// One pass over the keys, 64 at a time, with the running maximum and sum of the softmax (see attn_decode), on
+// v_mfma_f32_32x32x16_bf16: lane (j, r) = (lane / 32, lane % 32) holds eight inputs, 8 j .. 8 j + 7 of 16, of
+// row (or column) r, and rows 8 (i / 4) + 4 j + i % 4, i < 16, of column r of the result.
+//  - scores of keys x rows: K is the first operand, so lane (j, r) gets row r's scores, and maxima and sums
+//    of a row are those of two lanes;
+//  - output of dims x rows: V, transposed, is the first operand, and the scores are the second one as they
+//    are: registers 8 h .. 8 h + 7 of a 32-key tile are the 16 keys 16 h + 8 (e / 4) + 4 j + e % 4, e < 8, in
+//    an order that V's transposing reads (ds_read_b64_tr_b16, four keys of a dim to a lane) follow.
+// A wave has 32 rows, four waves share the keys' tiles in LDS; the next tile is sent for before one is used.
+#include <algorithm>
+
+#include "ql_attn.hpp"
+#include "ql_mx4.hpp"
+
+namespace ql {
+namespace {
+
+constexpr int kTileRows = 128, kTileKeys = 64;
+constexpr int kMinSplit = 8;     // tiles of keys of a part at least
+constexpr float kLag = 8.0f;     // how far (in powers of two) scores may pass the maximum in use
+
+struct PromptPlan {
+  int G, splits;
+  int64_t tiles;  // row tiles of a kv head at most
+};
+PromptPlan plan_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t keys) {
+  PromptPlan p;
+  p.G = (int)(Hq / Hkv);
+  p.tiles = T * p.G / kTileRows + B;
+  // Two workgroups fit a CU: where the rows do not make that many, the keys are split.
+  const int64_t blocks = (T * p.G + kTileRows - 1) / kTileRows * Hkv;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({768 / blocks, keys / (kMinSplit * kTileKeys), 32}));
+  return p;
+}
+
+struct RowTile {
+  int b, first, n, len, row0;  // sequence, its first row of q, queries, cached tokens, first (query, head) of the tile
+};
+__device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
+__device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want) {
+  const int lane = threadIdx.x & 63;
+  uint32_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int b = b0 + lane;
+    int first = 0, n = 0;
+    if (b < a.B) {
+      first = clamp_to(a.starts[b], 0, a.T);
+      n = clamp_to(a.starts[b + 1], first, a.T) - first;
+    }
+    const uint32_t upto = before + scan_lanes((uint32_t)(n * G + kTileRows - 1) / kTileRows);
+    const uint64_t here = __ballot((uint32_t)want < upto);
+    if (here) {
+      const int l = __builtin_ctzll(here);
+      RowTile t;
+      t.b = b0 + l;
+      t.first = __builtin_amdgcn_readlane(first, l);
+      t.n = __builtin_amdgcn_readlane(n, l);
+      t.len = clamp_to(a.lens[t.b], 0, a.keys);
+      // the longest rows first
+      t.row0 = (__builtin_amdgcn_readlane((int)upto, l) - 1 - want) * kTileRows;
+      return t;
+    }
+    before = last_lane(upto);
+  }
+  return RowTile{-1, 0, 0, 0, 0};
+}
+
+// the tiles of keys of a row tile, and of one of its parts
+struct Keys {
+  int tiles, per;
+  __device__ __forceinline__ Keys(const RowTile& t, int G, int splits) {
+    const int last = min((t.row0 + kTileRows - 1) / G, t.n - 1);
+    tiles = (max(t.len - t.n + last + 1, 0) + kTileKeys - 1) / kTileKeys;
+    per = max((tiles + splits - 1) / splits, kMinSplit);
+  }
+  __device__ __forceinline__ int parts() const { return max(1, (tiles + per - 1) / per); }
+};
+
+typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((address_space(3))) s16x4_t* ls16x4p;
+
+// Where 16-byte column c of a key's row lies in LDS, so that neither K's reads (16 bytes of 16 keys at a time)
+// nor V's (32 bytes of four keys) meet in a bank
+template <int D> __device__ __forceinline__ int swizzle_k(int key) { return key & (D / 8 - 1); }
+template <int D> __device__ __forceinline__ int swizzle_v(int key) { return 2 * (key & (D / 16 - 1)); }
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptPlan plan) {
+  constexpr int ROW = 2 * D, TILE = kTileKeys * ROW;  // bytes
+  constexpr int DK = D / 16, DT = D / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * TILE];  // K, V, K, V
+  __shared__ uint32_t odd_bits[2][kTileKeys][DT], odd_waves[4];
+  const int lane = threadIdx.x & 63, j = lane >> 5, r = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int Hkv = a.kv.heads, G = plan.G;
+  const int split = blockIdx.x % plan.splits, unit = blockIdx.x / plan.splits, head = unit % Hkv;
+  const RowTile rt = find_tile(a, G, unit / Hkv);
+  if (rt.b < 0) return;
+  const Keys keys(rt, G, plan.splits);
+  const int t0 = split * keys.per, t1 = min(keys.tiles, t0 + keys.per);
+  if (split && t0 >= t1) return;
+  const bool whole = keys.parts() == 1;
+
+  const int rows = rt.n * G - rt.row0;  // those of the tile, or more
+  const int base_pos = rt.len - rt.n + 1;
+  const int mine = min(wave * 32 + r, rows - 1) + rt.row0;
+  const int limit = base_pos + mine / G;  // keys that this row sees
+  const int limit_first = base_pos + min(rt.row0 + wave * 32, rt.n * G - 1) / G;
+  const int limit_tile = base_pos + rt.row0 / G;
+  const int limit_last = base_pos + min(rt.row0 + wave * 32 + 31, rt.n * G - 1) / G;
+
+  u32x4_t qf[DK];
+  {
+    const uint16_t* p = a.q + ((int64_t)(rt.first + mine / G) * a.Hq + (int64_t)head * G + mine % G) * D + 8 * j;
+#pragma unroll
+    for (int i = 0; i < DK; ++i) qf[i] = *(gu32x4p)(p + 16 * i);
+  }
+  const float c = a.score_scale * (a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
+
+  const int32_t* __restrict__ row = a.table + rt.b * a.table_stride;
+  const int shift = a.kv.page_shift;
+  const uint32_t in_page = (1u << shift) - 1;
+  const uint32_t lds0 = lds_offset(smem);
+  // Entries of a tile's four groups of 16 keys; wave w brings group w.  A group behind the last key takes the last
+  // key's page; entries that are no page read page 0 and are masked (bit g of the result).
+  const int key_last = max(1, min(rt.len, kTileKeys * keys.tiles)) - 1;
+  struct Source { const uint8_t *k, *v; int bad; };
+  auto source = [&](int t) {
+    Source s{nullptr, nullptr, 0};
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int key = t * kTileKeys + 16 * g, e = row[min(key, key_last) >> shift];
+      const bool ok = (uint32_t)e < (uint32_t)a.kv.pages;
+      s.bad |= ok ? 0 : 1 << g;
+      if (g == wave) {
+        const int64_t off = ((((int64_t)(ok ? e : 0) * Hkv + head) << shift) + (key & in_page)) * (int64_t)(F8 ? D : 2 * D);
+        s.k = a.kv.k + off, s.v = a.kv.v + off;
+      }
+    }
+    return s;
+  };
+  // bf16: straight into LDS, 1 KB (4 or 8 keys) an instruction
+  constexpr int PIECES = 16 * ROW / 1024, PER = 1024 / ROW;
+  auto send = [&](const Source& s, int buf) {
+    if constexpr (!F8) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int key = PER * i + lane / (64 / PER), col = lane % (64 / PER);
+        const uint32_t to = lds0 + buf * 2 * TILE + wave * 16 * ROW + i * 1024;
+        dma16(to, s.k, key * ROW + ((col ^ swizzle_k<D>(key)) * 16));
+        dma16(to + TILE, s.v, key * ROW + ((col ^ swizzle_v<D>(key)) * 16));
+      }
+    }
+  };
+  // e4m3: through registers, widened on the way
+  u32x4_t raw[2][F8 ? D / 64 : 1];
+  auto fetch = [&](const Source& s) {
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t off = lane / 4 * D + (lane % 4 + 4 * i) * 16;
+        raw[0][i] = *(gu32x4p)(s.k + off), raw[1][i] = *(gu32x4p)(s.v + off);
+      }
+    }
+  };
+  auto put = [&](int buf) {
+    if constexpr (F8) {
+      const int key = lane / 4;
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = 2 * (lane % 4 + 4 * i) + h;
+            const u32x2_t x = bf16_of_e4m3(raw[z][i][2 * h]), y = bf16_of_e4m3(raw[z][i][2 * h + 1]);
+            uint8_t* to = smem + buf * 2 * TILE + z * TILE + (wave * 16 + key) * ROW +
+                          (col ^ (z ? swizzle_v<D>(key) : swizzle_k<D>(key))) * 16;
+            *(u32x4_t*)to = u32x4_t{x[0], x[1], y[0], y[1]};
+          }
+    }
+  };
+  // four keys (from `key` on) of dim 32 dt + r
+  auto v_part = [&](const uint8_t* v, int dt, int key0) {
+    const int key = key0 + (lane & 15) / 4, d = 32 * dt + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    const uint8_t* p = v + key * ROW + ((d / 8) ^ swizzle_v<D>(key)) * 16 + (d % 8) * 2;
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4p)p));
+  };
+  auto v_frag = [&](const uint8_t* v, int dt, int cc) {
+    const u32x2_t lo = v_part(v, dt, 16 * cc + 4 * j), hi = v_part(v, dt, 16 * cc + 8 + 4 * j);
+    return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+  };
+  auto mfma = [](const u32x4_t& x, const u32x4_t& y, at_f32x16 z) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8, x), __builtin_bit_cast(at_bf16x8, y), z, 0, 0, 0);
+  };
+
+  float m = kNegInf, sum = 0.0f;
+  at_f32x16 o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+  uint32_t infinities[DT] = {};  // bit e: +inf to o[dt][e], 16 + e: -inf
+
+  Source next = {};
+  int bad = 0;
+  if (t0 < t1) {
+    next = source(t0);
+    send(next, 0);
+    fetch(next);
+    put(0);
+    bad = next.bad;
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1, key0 = t * kTileKeys;
+    const uint8_t *kt = smem + buf * 2 * TILE, *vt = kt + TILE;
+    wait_vm<0>();
+    wait_lgkm();
+    barrier();
+    const int bad_now = bad;
+    if (t + 1 < t1) {
+      next = source(t + 1);
+      send(next, buf ^ 1);
+      fetch(next);
+      bad = next.bad;
+    }
+    // 0 * inf is NaN, also where a weight is 0 because the row does not see the key, and what memory behind the
+    // last key holds is anything.  So in tiles that not every row sees whole, values that are not finite are taken
+    // out of V, and noted: bit d % 32 of word d / 32 of a key, for +inf, -inf and (both) NaN.
+    bool odd = false;
+    if (key0 + kTileKeys > limit_tile || bad_now) {
+      const int key = threadIdx.x / DT, dt = threadIdx.x % DT;
+      bool found = false;
+      if (key < kTileKeys) {
+        uint32_t up = 0, down = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u32x4_t* at = (u32x4_t*)(smem + buf * 2 * TILE + TILE + key * ROW + ((4 * dt + i) ^ swizzle_v<D>(key)) * 16);
+          u32x4_t v = *at;
+          uint32_t most = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) most = max(most, max(v[e] & 0x7FFFu, v[e] >> 16 & 0x7FFFu));
+          if (most >= 0x7F80u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t x = v[e] >> (16 * h) & 0xFFFFu;
+                if ((x & 0x7FFFu) < 0x7F80u) continue;
+                up |= x != 0xFF80u ? 1u << (8 * i + 2 * e + h) : 0u;
+                down |= x != 0x7F80u ? 1u << (8 * i + 2 * e + h) : 0u;
+                v[e] &= h ? 0x0000FFFFu : 0xFFFF0000u;
+              }
+            *at = v;
+            found = true;
+          }
+        }
+        odd_bits[0][key][dt] = up, odd_bits[1][key][dt] = down;
+      }
+      const bool any = __ballot(found) != 0;
+      if (lane == 0) odd_waves[wave] = any;
+      __syncthreads();
+      odd = odd_waves[0] | odd_waves[1] | odd_waves[2] | odd_waves[3];
+    }
+    if (key0 < limit_last) {
+      at_f32x16 s[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[z][e] = 0.0f;
+        const int key = 32 * z + r;
+#pragma unroll
+        for (int i = 0; i < DK; ++i) {
+          const u32x4_t kf = *(lu32x4p)(kt + key * ROW + (((2 * i + j) ^ swizzle_k<D>(key)) * 16));
+          s[z] = mfma(kf, qf[i], s[z]);
+        }
+      }
+      const bool masked = key0 + kTileKeys > limit_first || bad_now;
+      if (masked) {
+        const int visible = limit - key0 - 4 * j;
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const bool sees = 32 * z + 8 * (e / 4) + e % 4 < visible && !(bad_now >> (2 * z + e / 8) & 1);
+            s[z][e] = sees ? s[z][e] : kNegInf;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
+      top = max_xor32(top) * c;
+      // The maximum in use follows only when some row's scores pass it by 2^kLag (the result is the same: it
+      // cancels out, and sums of exp2 below 2^8 each keep far from fp32's end)
+      if (__ballot(top > m + kLag)) {
+        const float m_new = fmaxf(m, top), alpha = part_weight(m, m_new);
+        m = m_new;
+        sum *= alpha;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
+      }
+      const float base = m == kNegInf ? 0.0f : m;
+      u32x4_t pf[4];
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = exp2_fast(__builtin_fmaf(s[cc / 2][8 * (cc % 2) + e], c, -base));
+          sum += p[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pf[cc][e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+      }
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[dt] = mfma(v_frag(vt, dt, cc), pf[cc], o[dt]);
+      if (__builtin_expect(odd, 0)) {  // which of the lane's sums what was taken out belongs to
+        for (int key = 0; key < kTileKeys; ++key) {
+          if (key0 + key >= limit || (bad_now >> (key / 16) & 1)) continue;
+#pragma unroll
+          for (int i = 0; i < 2 * DT; ++i) {
+            uint32_t w = odd_bits[i % 2][key][i / 2] >> (4 * j) & 0x0F0F0F0Fu;
+            w = (w | w >> 4) & 0x00FF00FFu;
+            infinities[i / 2] |= ((w | w >> 8) & 0xFFFFu) << (16 * (i % 2));
+          }
+        }
+      }
+    }
+    if (t + 1 < t1) put(buf ^ 1);
+  }
+  wait_vm<0>();
+
+  sum = sum_xor32(sum);
+  if (wave * 32 + r >= rows) return;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+    if (infinities[dt]) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        o[dt][e] += infinities[dt] >> e & 1 ? -kNegInf : 0.0f;
+        o[dt][e] += infinities[dt] >> (16 + e) & 1 ? kNegInf : 0.0f;
+      }
+    }
+  if (whole) {
+    const float inv = sum == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / sum;
+    uint16_t* out = a.out + ((int64_t)(rt.first + mine / G) * a.Hq + (int64_t)head * G + mine % G) * D;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *(u32x2_t*)(out + 32 * dt + 2 * e + 4 * j) =
+            u32x2_t{pack_bf16(o[dt][e] * inv, o[dt][e + 1] * inv), pack_bf16(o[dt][e + 2] * inv, o[dt][e + 3] * inv)};
+  } else {
+    const int64_t at = ((int64_t)unit * plan.splits + split) * kTileRows + wave * 32 + r;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *(at_f32x4*)(a.ws + at * D + 32 * dt + 2 * e + 4 * j) = at_f32x4{o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]};
+    if (j == 0) *(float2*)(a.ws + plan.tiles * Hkv * plan.splits * kTileRows * D + at * 2) = make_float2(m, sum);
+  }
+}
+
+// The parts' sums, weighed by their maxima, in their order: D / 4 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, PromptPlan plan) {
+  constexpr int LANES = D / 4, ROWS = 256 / LANES;
+  const int Hkv = a.kv.heads, G = plan.G, unit = blockIdx.x, head = unit % Hkv;
+  const RowTile rt = find_tile(a, G, unit / Hkv);
+  if (rt.b < 0) return;
+  const Keys keys(rt, G, plan.splits);
+  const int parts = keys.parts(), l = threadIdx.x % LANES, row = blockIdx.y * ROWS + threadIdx.x / LANES;
+  if (parts == 1 || row >= rt.n * G - rt.row0) return;
+  const float* __restrict__ stats = a.ws + plan.tiles * Hkv * plan.splits * kTileRows * D;
+  auto slot = [&](int s) { return ((int64_t)unit * plan.splits + s) * kTileRows + row; };
+  float most = kNegInf;
+  for (int s = 0; s < parts; ++s) most = fmaxf(most, stats[2 * slot(s)]);
+  at_f32x4 y{0, 0, 0, 0};
+  float total = 0.0f;
+  for (int s = 0; s < parts; ++s) {
+    const float f = part_weight(stats[2 * slot(s)], most);
+    total += f * stats[2 * slot(s) + 1];
+    const at_f32x4 v = *(const at_f32x4*)(a.ws + slot(s) * D + 4 * l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += f * v[i];
+  }
+  const float inv = total == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / total;
+  const int mine = rt.row0 + row;
+  *(u32x2_t*)(a.out + ((int64_t)(rt.first + mine / G) * a.Hq + (int64_t)head * G + mine % G) * D + 4 * l) =
+      u32x2_t{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+}
+
+template <int D>
+void launch(const AttnArgs& a, const PromptPlan& p, hipStream_t stream) {
+  const uint32_t blocks = (uint32_t)(p.tiles * a.kv.heads);
+  if (a.kv.f8) attn_prompt_kernel<D, true><<<blocks * p.splits, 256, 0, stream>>>(a, p);
+  else attn_prompt_kernel<D, false><<<blocks * p.splits, 256, 0, stream>>>(a, p);
+  if (p.splits > 1) attn_prompt_join_kernel<D><<<dim3(blocks, kTileRows * D / 1024), 256, 0, stream>>>(a, p);
+}
+
+}  // namespace
+
+size_t attn_prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys) {
+  const PromptPlan p = plan_of(T, B, Hq, Hkv, keys);
+  return p.splits > 1 ? (size_t)(p.tiles * Hkv * p.splits * kTileRows * (D + 2)) * sizeof(float) : 0;
+}
+int64_t attn_prompt_blocks(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t, int64_t keys) {
+  const PromptPlan p = plan_of(T, B, Hq, Hkv, keys);
+  return p.tiles * Hkv * p.splits;
+}
+
+hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t stream) {
+  const PromptPlan p = plan_of(a.T, a.B, a.Hq, a.kv.heads, a.keys);
+  if (a.kv.dim == 64) launch<64>(a, p, stream);
+  else launch<128>(a, p, stream);
+  return hipGetLastError();
+}
+
+}  // namespace ql

@@ -64,6 +64,17 @@ class ql_mx4_experts(ctypes.Structure):
                 ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
 
 
+class ql_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("page", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class ql_rope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 def lib():
     """Load libqlinear.so; raise if it has not been built."""
     global _lib
@@ -142,6 +153,16 @@ def lib():
         L.qlinear_mx4_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
         L.qlinear_mx4_moe_workspace_bytes.restype = sz
         L.qlinear_mx4_moe.argtypes = [vp, i64, vp, vp, vp, sz, vp]
+        f32 = ctypes.c_float
+        L.qlinear_rope_append.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, f32, vp, vp, vp]
+        L.qlinear_attn_decode_workspace_bytes.argtypes = [i64] * 5
+        L.qlinear_attn_decode_workspace_bytes.restype = sz
+        L.qlinear_attn_decode.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, f32, vp, vp, sz, vp]
+        L.qlinear_attn_prompt_workspace_bytes.argtypes = [i64] * 6
+        L.qlinear_attn_prompt_workspace_bytes.restype = sz
+        L.qlinear_attn_prompt.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, i64, vp, f32, vp, vp, sz, vp]
+        for name in ("qlinear_rope_append", "qlinear_attn_decode", "qlinear_attn_prompt"):
+            getattr(L, name).restype = i32
         for name in ("qlinear_mx4_quantize", "qlinear_mx4_dequant", "qlinear_mx4_gemv", "qlinear_mx4_gemm",
                      "qlinear_moe_route", "qlinear_mx4_moe"):
             getattr(L, name).restype = i32
@@ -764,6 +785,205 @@ def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4
                        up.codes.data_ptr(), up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr())
     _launch("mx4_moe", lib().qlinear_mx4_moe, device, ctypes.byref(e), T, x.data_ptr(), out.data_ptr(),
             workspace.data_ptr(), need)
+    return out
+
+
+# ---------------------------------------------------------------- rotary positions and attention
+@dataclass(frozen=True, eq=False)
+class KvCache:
+    """A paged key-value cache: k, v [pages, heads, page, D], bf16, or float8_e4m3fn with one scale per head (a
+    stored x stands for x * scale).  Slot number i is place i % page of page i // page."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: Optional[torch.Tensor] = None  # fp32 [heads], positive; e4m3 only
+    v_scale: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        if k.dtype not in _CACHE_TYPES or v.dtype != k.dtype:
+            raise ValueError(f"k and v must be both bfloat16 or both float8_e4m3fn, got {k.dtype} and {v.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or not k.numel():
+            raise ValueError(f"k and v must be [pages, heads, page, D], got {tuple(k.shape)} and {tuple(v.shape)}")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous")
+        pages, heads, page, D = k.shape
+        if D not in (64, 128):
+            raise ValueError(f"heads must have 64 or 128 dims, got {D}")
+        if not 16 <= page <= 4096 or page & (page - 1):
+            raise ValueError(f"a page must hold 16..4096 tokens, a power of two, got {page}")
+        for s, name in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
+            if k.dtype == torch.bfloat16:
+                if s is not None:
+                    raise ValueError(f"{name}: a bfloat16 cache has no scales")
+            elif s is None or s.dtype != torch.float32 or s.shape != (heads,) or not s.is_contiguous() or \
+                    s.device != k.device:
+                raise ValueError(f"{name} must be float32 [{heads}], contiguous, on the cache's device")
+        if v.device != k.device:
+            raise ValueError("k and v must be on one device")
+        object.__setattr__(self, "shape", (pages, heads, page, D))
+        object.__setattr__(self, "desc", ql_kv_cache(
+            pages, heads, page, D, _CACHE_TYPES[k.dtype], 0, k.data_ptr(), v.data_ptr(),
+            None if self.k_scale is None else self.k_scale.data_ptr(),
+            None if self.v_scale is None else self.v_scale.data_ptr()))
+
+    @property
+    def nbytes(self) -> int:
+        """Stored bytes of k and v."""
+        return 2 * self.k.numel() * self.k.element_size()
+
+
+_CACHE_TYPES = {torch.bfloat16: 1, torch.float8_e4m3fn: 3}  # ql_dtype
+
+
+@dataclass(frozen=True, eq=False)
+class Rope:
+    """Rotary positions of the first 2 * len(freqs) dims of a head: pair p is turned by position * freqs[p] (fp32,
+    on the device) and scaled by factor.  Pairs are dims p and p + len(freqs), or (interleaved) 2p and 2p + 1."""
+    freqs: torch.Tensor
+    interleaved: bool = False
+    factor: float = 1.0
+
+    def __post_init__(self):
+        f = self.freqs
+        if f.dtype != torch.float32 or f.dim() != 1 or not f.numel() or not f.is_contiguous():
+            raise ValueError("freqs must be float32 [pairs], contiguous")
+        object.__setattr__(self, "desc", ql_rope(f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0,
+                                                 float(self.factor), 0))
+
+
+def rope_frequencies(dims: int, base: float = 10000.0, stretch: float = 1.0, original: Optional[int] = None,
+                     fast: float = 32.0, slow: float = 1.0) -> tuple[torch.Tensor, float]:
+    """(freqs fp32 [dims / 2] on the host, factor) for a Rope of `dims` dims: base^(-2p / dims), for contexts
+    `stretch` times as long divided by stretch (positions squeezed linearly) or, with the `original` context
+    length, by parts: pairs that turn more than `fast` times within it keep their frequency, those that turn
+    less than `slow` times are divided by stretch, the ones between are mixed by a ramp over the pairs' number,
+    and factor is 0.1 ln(stretch) + 1."""
+    if dims < 2 or dims % 2 or not base > 1 or not stretch >= 1 or not fast > slow > 0 or \
+            (original is not None and original < 1):
+        raise ValueError("an even number of dims, base > 1, stretch >= 1, fast > slow > 0, original >= 1")
+    p = np.arange(dims // 2, dtype=np.float64)
+    f = float(base) ** (-2 * p / dims)
+    if original is None or stretch == 1:
+        return torch.from_numpy((f / stretch).astype(np.float32)), 1.0
+
+    def pair(turns):  # whose frequency makes that many turns in `original` tokens
+        return dims * np.log(original / (turns * 2 * np.pi)) / (2 * np.log(base))
+
+    low = max(np.floor(pair(fast)), 0)
+    high = min(np.ceil(pair(slow)), dims - 1)
+    ramp = np.clip((p - low) / max(high - low, 0.001), 0, 1)
+    f = f / stretch * ramp + f * (1 - ramp)
+    return torch.from_numpy(f.astype(np.float32)), 0.1 * float(np.log(stretch)) + 1.0
+
+
+def _int32(t: torch.Tensor, shape: tuple, device: torch.device, name: str):
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be int32 {list(shape)}, contiguous, on {device}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _cache(cache: KvCache, device: torch.device):
+    if not isinstance(cache, KvCache):
+        raise ValueError("cache must be a KvCache")
+    if cache.k.device != device:
+        raise ValueError("the cache must be on the device of the other operands, a CUDA (HIP) device")
+    return ctypes.byref(cache.desc)
+
+
+def _heads(x: torch.Tensor, D: int, name: str) -> int:
+    """The heads of x [T, heads, D] or [T, heads * D], rows at any distance."""
+    if x.dim() == 3:
+        if x.shape[2] == D and x.stride(2) == 1 and (x.stride(1) == D or x.shape[1] == 1):
+            return x.shape[1]
+    elif x.dim() == 2 and x.shape[1] % D == 0 and x.stride(1) == 1:
+        return x.shape[1] // D
+    raise ValueError(f"{name} must be [T, heads, {D}] or [T, heads * {D}] with contiguous rows, got {tuple(x.shape)}")
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                rope: Rope, cache: KvCache, q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """q turned by its tokens' positions, bf16 of q's shape; k, turned, and v go to the cache's slots.
+    q [T, Hq, D] or [T, Hq * D], k and v alike with the cache's heads (fp32, bf16 or fp16, all of one type; rows
+    may be parts of wider ones); positions, slots int32 [T], a slot outside the cache (-1) is not written, and no
+    slot may appear twice.  q_norm, k_norm (fp32 [D]): x * norm / sqrt(mean x^2 + eps) over each head first."""
+    device = q.device
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA (HIP) tensor")
+    desc = _cache(cache, device)
+    if q.dtype not in _DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError(f"q, k and v must be all float32, bfloat16 or float16, got {q.dtype}, {k.dtype}, {v.dtype}")
+    _, Hkv, _, D = cache.shape
+    Hq = _heads(q, D, "q")
+    T = q.shape[0]
+    if _heads(k, D, "k") != Hkv or _heads(v, D, "v") != Hkv or k.shape[0] != T or v.shape[0] != T or \
+            k.device != device or v.device != device:
+        raise ValueError(f"k and v must be [{T}, {Hkv}, {D}] on {device}")
+    if not isinstance(rope, Rope) or rope.freqs.device != device:
+        raise ValueError(f"rope must be a Rope with its frequencies on {device}")
+    norms = [None, None]
+    for i, n in enumerate((q_norm, k_norm)):
+        if n is not None:
+            if n.dtype != torch.float32 or n.shape != (D,) or n.device != device or not n.is_contiguous():
+                raise ValueError(f"{'qk'[i]}_norm must be float32 [{D}] on {device}")
+            norms[i] = n.data_ptr()
+    pos, slot = _int32(positions, (T,), device, "positions"), _int32(slots, (T,), device, "slots")
+    out = _result(out, q.shape, torch.bfloat16, device)
+    _launch("rope_append", lib().qlinear_rope_append, device, T, Hq, _DTYPES[q.dtype], q.data_ptr(), q.stride(0),
+            k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), pos, slot, ctypes.byref(rope.desc), norms[0], norms[1],
+            eps, desc, out.data_ptr())
+    return out
+
+
+def _attention(q, cache, table, lens, scale):
+    """Checks both attentions make: (device, cache's descriptor, rows, Hq, sequences, pages of a row, scale)."""
+    device = q.device
+    _dev(q, torch.bfloat16, "q")
+    desc = _cache(cache, device)
+    D = cache.shape[3]
+    Hq = _heads(q, D, "q")
+    if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1 and table.shape[1] != 1 or \
+            table.device != device:
+        raise ValueError(f"table must be int32 [B, pages of a sequence] on {device}, its rows contiguous")
+    B, most = table.shape
+    _int32(lens, (B,), device, "lens")
+    return device, desc, q.shape[0], Hq, B, most, D ** -0.5 if scale is None else float(scale)
+
+
+def attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lens: torch.Tensor, scale: Optional[float] = None,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of one new token per sequence, bf16 of q's shape: q [B, Hq, D] or [B, Hq * D] bf16 over the first
+    lens[b] tokens (int32 [B]; 0: the result is 0) in the pages that table[b] (int32 [B, pages]) names in order.
+    Hq is a multiple of the cache's heads; entries that are no page stand for tokens that are not seen.
+    scale: of the scores, D ** -0.5 unless given."""
+    device, desc, rows, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
+    if rows != B:
+        raise ValueError(f"q has {rows} rows, the table {B}")
+    out = _result(out, q.shape, torch.bfloat16, device)
+    _, Hkv, page, D = cache.shape
+    need = _workspace_bytes("attn_decode", device, B, Hq, Hkv, D, most * page)
+    workspace = _scratch(workspace, need, device) if need else None
+    _launch("attn_decode", lib().qlinear_attn_decode, device, desc, B, Hq, q.data_ptr(), table.data_ptr(),
+            table.stride(0), most, lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr() if need else None, need)
+    return out
+
+
+def attn_prompt(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, table: torch.Tensor, lens: torch.Tensor,
+                scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of packed prompts (or their next chunks), bf16 of q's shape: rows starts[b] .. starts[b + 1]
+    of q [T, Hq, D] or [T, Hq * D] bf16 (starts int32 [B + 1], ascending) are the last tokens of sequence b, whose
+    lens[b] tokens (those rows' included) are in the pages of table[b].  Row i of n sees tokens 0 .. lens[b] - n + i;
+    one that sees none gives 0; rows that belong to no sequence are not written.  The rest as for attn_decode."""
+    device, desc, T, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
+    _int32(starts, (B + 1,), device, "starts")
+    out = _result(out, q.shape, torch.bfloat16, device)
+    _, Hkv, page, D = cache.shape
+    need = _workspace_bytes("attn_prompt", device, T, B, Hq, Hkv, D, most * page)
+    workspace = _scratch(workspace, need, device) if need else None
+    _launch("attn_prompt", lib().qlinear_attn_prompt, device, desc, T, B, Hq, q.data_ptr(), starts.data_ptr(),
+            table.data_ptr(), table.stride(0), most, lens.data_ptr(), scale, out.data_ptr(),
+            workspace.data_ptr() if need else None, need)
     return out
 
 

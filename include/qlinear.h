@@ -402,8 +402,9 @@ ql_status qlinear_lb_gemv(const ql_littlebit *w, const uint16_t *x, float *y, vo
  * A stack of matrices (experts) is a matrix with count*N rows.  N*K is at most 2^36 elements
  * and K at most 2^26; the products take N below 2^26 and K up to 2^24. */
 
-/* Element types of inputs that may come in several. */
-typedef enum { QL_F32 = 0, QL_BF16 = 1, QL_F16 = 2 } ql_dtype;
+/* Element types of inputs that may come in several.  QL_E4M3 (8-bit floats of 4 exponent and 3 mantissa
+ * bits, no infinities, largest 448) is for the key-value cache alone. */
+typedef enum { QL_F32 = 0, QL_BF16 = 1, QL_F16 = 2, QL_E4M3 = 3 } ql_dtype;
 
 /* Bytes of one row of scales, 4 * ceil(K / 128); 0 if K is invalid. */
 int64_t qlinear_mx4_scale_stride(int64_t K);
@@ -482,6 +483,74 @@ typedef struct {
 size_t qlinear_mx4_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 ql_status qlinear_mx4_moe(const ql_mx4_experts *experts, int64_t T, const uint16_t *x, float *y, void *workspace,
                           size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------- rotary positions and attention
+ *
+ * What a decoder layer does between its q, k, v products and its output product: qlinear_rope_append takes
+ * the products' rows, qlinear_attn_decode and qlinear_attn_prompt return rows of bf16 as the products take
+ * them.  The key-value cache between them is in pages, of any order in memory:
+ *   k, v (dev) [pages][heads][page][dim] of type QL_BF16, or QL_E4M3 with one fp32 scale per head, (dev)
+ *   [heads], positive: a stored x stands for x * scale.  Scales are NULL for QL_BF16.
+ * Slot number i is place i % page of page i / page.  dim is 64 or 128; page a power of two, 16 .. 4096;
+ * pages * page is below 2^31.  Arrays of int32 and small fp32 ones (scales, norms, freqs) need an alignment
+ * of 4 bytes only.  Values that are not finite are taken as they are: a row that sees them is not finite, the others
+ * are as without them. */
+typedef struct {
+  int32_t pages, heads, page, dim;
+  int32_t type; /* ql_dtype: QL_BF16 or QL_E4M3 */
+  int32_t reserved;
+  void *k, *v;                    /* (dev) */
+  const float *k_scale, *v_scale; /* (dev) [heads], or NULL */
+} ql_kv_cache;
+
+/* Rotary positions of the first `dims` (even, 2 .. dim) dims of a head: pair p is turned by the angle
+ * position * freqs[p], and scaled by `factor`.  A pair is dims p and p + dims / 2, or (interleaved) 2p and
+ * 2p + 1:  (u, v) -> factor * (u cos - v sin, v cos + u sin).  Angles are products in 64 bits. */
+typedef struct {
+  const float *freqs; /* (dev) [dims / 2] */
+  int32_t dims, interleaved;
+  float factor;
+  int32_t reserved;
+} ql_rope;
+
+/* q [T][Hq][dim], k and v [T][heads][dim] of type dtype (QL_F32, QL_BF16, QL_F16), token t at t * stride
+ * elements (a multiple of 16 bytes, so they may be parts of one wider row): q and k are normed if q_norm /
+ * k_norm are not NULL (x * norm / sqrt(mean of the head's x^2 + eps), norm (dev) fp32 [dim]) and turned; q is
+ * written to out (dev) bf16 bits [T][Hq][dim], k and v to slot slots[t] of the cache (e4m3: x / scale, what is
+ * over 448 as 448).  A slot that is not in the cache (-1: a padded token) is left out; no slot may appear twice.
+ *   positions, slots (dev) int32 [T]; 1 <= T < 2^24. */
+ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void *q, int64_t q_stride, const void *k,
+                              int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                              const int32_t *slots, const ql_rope *rope, const float *q_norm, const float *k_norm,
+                              float eps, const ql_kv_cache *cache, uint16_t *out, hipStream_t stream);
+
+/* Attention of one new token of each of B sequences: out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
+ * over the first lens[b] tokens of row b of the table, kv head h / (Hq / heads).  The table's row names the
+ * sequence's pages in order.  A sequence of no tokens gives 0; lengths are cut to what a row of the table
+ * holds; entries that are no page of the cache stand for tokens that are not seen.  What memory behind a
+ * sequence's last token holds does not matter.  Softmax statistics and sums are fp32, its weights bf16 as
+ * they enter the second product.  Deterministic for given B, lens and heads.
+ *   q (dev) bf16 bits [B][Hq][dim]; table (dev) int32 [B][max_pages], row b at b * table_stride; lens (dev)
+ *   int32 [B]; scale > 0; out (dev) bf16 bits [B][Hq][dim]; workspace (dev, 16-byte aligned, contents need not
+ *   be zeroed) of qlinear_attn_decode_workspace_bytes, the parts of long sequences; 0 (then NULL will do) if
+ *   rows of the table are short.  Calls that share a workspace must not overlap.
+ * Hq is a multiple of heads; max_pages * page is below 2^31 (keys, in the size). */
+size_t qlinear_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys);
+ql_status qlinear_attn_decode(const ql_kv_cache *cache, int64_t B, int64_t Hq, const uint16_t *q,
+                              const int32_t *table, int64_t table_stride, int64_t max_pages, const int32_t *lens,
+                              float scale, uint16_t *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Causal attention of packed prompts, or of prompts' next chunks: sequence b's n = starts[b + 1] - starts[b]
+ * queries are rows starts[b] .. of q and out, and stand for the last n of its lens[b] tokens, which the cache
+ * holds already: query i sees tokens 0 .. lens[b] - n + i (none: 0 comes out, where lens[b] < n).  Rows that
+ * belong to no sequence are not written.  All else as for qlinear_attn_decode.
+ *   q, out (dev) bf16 bits [T][Hq][dim]; starts (dev) int32 [B + 1], ascending, cut to 0 .. T; T * Hq is below
+ *   2^31; workspace of qlinear_attn_prompt_workspace_bytes, where few rows meet many keys, else 0. */
+size_t qlinear_attn_prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys);
+ql_status qlinear_attn_prompt(const ql_kv_cache *cache, int64_t T, int64_t B, int64_t Hq, const uint16_t *q,
+                              const int32_t *starts, const int32_t *table, int64_t table_stride, int64_t max_pages,
+                              const int32_t *lens, float scale, uint16_t *out, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------- 4-bit container baseline
  *
