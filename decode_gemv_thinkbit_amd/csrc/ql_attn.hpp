@@ -55,6 +55,10 @@ constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// what a call reads once: not kept in the caches
+template <class P>
+__device__ __forceinline__ auto load_once(P p) { return __builtin_nontemporal_load(p); }
+
 // two fp32 as a dword of bf16, the first in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef __attribute__((ext_vector_type(2))) __bf16 bf2;

@@ -20,40 +20,44 @@
 namespace ql {
 namespace {
 
-constexpr int kStep = 32;        // keys of a wave's step
-constexpr int kChunkStep = 128;  // a chunk's keys are a multiple: one step of each of the four waves
-constexpr int kMinChunk = 256;   // keys of a chunk at least
-constexpr int kRows = 16;        // heads a workgroup takes at most
+constexpr int kWaves = 4;
+constexpr int kStep = 32;                    // keys of a wave's step
+constexpr int kChunkStep = kWaves * kStep;   // a chunk's keys are a multiple: one step of each wave
+constexpr int kWhole = 512;                  // where no sequence can have more keys, each is one chunk
+constexpr int kTarget = 1024;                // chunks of a call, about: four workgroups for each CU
+constexpr int kRows = 16;                    // heads a workgroup takes at most
 
 // Work is cut on the device, where the lengths are: chunks of equal length C over all sequences, C the least
-// (a multiple of kChunkStep) for which the grid, `target` + one for each sequence and head, holds them all.
+// (a multiple of kChunkStep) for which the grid, kTarget + one for each sequence and head, holds them all.
 // Every wave finds its place by itself, 64 sequences at a time.
 struct Place {
-  int b, chunk, chunks, first, len, size;  // first: the number of b's first chunk; size: keys of a chunk
+  int b, len, chunk, chunks, first, size;  // first: the number of b's first chunk; size: keys of a chunk
 };
 __device__ __forceinline__ int clamp_len(int len, int keys) { return len < 0 ? 0 : len > keys ? keys : len; }
 
-template <bool BY_SEQUENCE>  // else by chunk number `want`
-__device__ __forceinline__ Place find_place(const int32_t* __restrict__ lens, int B, int keys, int heads, int target, int want) {
+template <bool BY_SEQUENCE>  // sequence `want`, or the one that has chunk number `want` (b < 0: none)
+__device__ __forceinline__ Place find_place(const int32_t* __restrict__ lens, int B, int keys, int heads, int want) {
   const int lane = threadIdx.x & 63;
-  auto units = [&](int b) { return b < B ? (uint32_t)max(1, (clamp_len(lens[b], keys) + kChunkStep - 1) / kChunkStep) : 0u; };
-  uint32_t mine = units(lane), total = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) total += last_lane(scan_lanes(b0 ? units(b0 + lane) : mine));
-  const uint64_t share = ((uint64_t)total * (uint32_t)heads + (uint32_t)target - 1) / (uint32_t)target;
-  const uint32_t c = max((uint32_t)share, (uint32_t)(kMinChunk / kChunkStep));
+  auto length = [&](int b) { return b < B ? clamp_len(lens[b], keys) : -1; };
+  auto steps = [&](int len) { return len < 0 ? 0u : max(1u, ((uint32_t)len + kChunkStep - 1) / kChunkStep); };
+  const int len0 = length(lane);
+  uint32_t total = last_lane(scan_lanes(steps(len0)));
+  for (int b0 = 64; b0 < B; b0 += 64) total += last_lane(scan_lanes(steps(length(b0 + lane))));
+  const uint32_t c = (uint32_t)(((uint64_t)total * (uint32_t)heads + kTarget - 1) / kTarget);
   uint32_t before = 0;
   for (int b0 = 0; b0 < B; b0 += 64) {
-    const uint32_t u = b0 ? units(b0 + lane) : mine, n = (u + c - 1) / c;
+    const int len = b0 ? length(b0 + lane) : len0;
+    const uint32_t n = (steps(len) + c - 1) / c;
     const uint32_t upto = before + scan_lanes(n);
     const uint64_t here = __ballot(BY_SEQUENCE ? b0 + lane == want : (uint32_t)want < upto);
     if (here) {
       const int l = __builtin_ctzll(here);
       Place p;
       p.b = b0 + l;
+      p.len = __builtin_amdgcn_readlane(len, l);
       p.chunks = __builtin_amdgcn_readlane((int)n, l);
       p.first = __builtin_amdgcn_readlane((int)upto, l) - p.chunks;
       p.chunk = BY_SEQUENCE ? 0 : want - p.first;
-      p.len = clamp_len(lens[p.b], keys);
       p.size = (int)c * kChunkStep;
       return p;
     }
@@ -63,42 +67,47 @@ __device__ __forceinline__ Place find_place(const int32_t* __restrict__ lens, in
 }
 
 struct Split {  // the grid of a call
-  int G, tiles, rows, heads, target;  // heads: kv heads x tiles of 16 of their q heads; rows: of a tile
+  int G, tiles, rows, heads;  // heads: kv heads x tiles of 16 of their q heads; rows: of a tile
   int64_t units;
 };
 Split split_of(int64_t B, int64_t Hq, int64_t Hkv) {
   Split s;
   s.G = (int)(Hq / Hkv), s.tiles = (s.G + kRows - 1) / kRows, s.rows = std::min(s.G, kRows);
   s.heads = (int)Hkv * s.tiles;
-  s.target = 1024;
-  s.units = s.target + B * s.heads;
+  s.units = kTarget + B * s.heads;
   return s;
 }
-bool may_split(int64_t keys) { return keys > kMinChunk; }
+bool may_split(int64_t keys) { return keys > kWhole; }
 
 // Partial results: [unit][row][D] sums of exp2(s - m) v, then [unit][row][2]: m, sum
 __device__ __forceinline__ int64_t stats_at(int64_t units, int rows, int D) { return units * rows * D; }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split sp) {
+template <int D, bool F8, bool SPLIT>
+__global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a, Split sp) {
   constexpr int ES = F8 ? 1 : 2;
   constexpr int KL = D * ES / 64;   // 16-byte loads of a key row by four lanes
   constexpr int NB = D / 16;        // dims of a lane in the second product, and its instructions
   constexpr int VD = NB * ES / 4;   // dwords of them as stored
   constexpr int NW = NB / 2;        // and as bf16
-  __shared__ __attribute__((aligned(16))) float part[4][kRows][D + 4];
-  __shared__ float stats[4][kRows][2];
+  __shared__ __attribute__((aligned(16))) float part[kWaves][kRows][D + 4];
+  __shared__ float stats[kWaves][kRows][2];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int unit = blockIdx.x, hk = unit % sp.heads, head = hk / sp.tiles, tile = hk % sp.tiles;
-  const Place at = find_place<false>(a.lens, a.B, a.keys, sp.heads, sp.target, unit / sp.heads);
-  if (at.b < 0) return;
+  Place at;
+  if constexpr (SPLIT) {
+    at = find_place<false>(a.lens, a.B, a.keys, sp.heads, unit / sp.heads);
+    if (at.b < 0) return;
+  } else {
+    const int b = unit / sp.heads, len = clamp_len(a.lens[b], a.keys);
+    at = Place{b, len, 0, 1, b, kWhole};
+  }
   const int begin = at.chunk * at.size, end = min(at.len, begin + at.size);
-  const int steps = (end - begin + kStep - 1) / kStep, mine = steps > wave ? (steps - wave + 3) / 4 : 0;
+  const int steps = (end - begin + kStep - 1) / kStep, mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
   const int rows = min(sp.rows, sp.G - tile * kRows);
 
   // q: column r, dims as K's bytes lie: 16 of a 64-byte piece to each lane
-  uint32_t qw[2 * KL * ES > 0 ? D / 32 : 1][4];
+  uint32_t qw[D / 32][4];
   {
     const uint16_t* p = a.q + ((int64_t)at.b * a.Hq + (int64_t)head * sp.G + tile * kRows + min(r, rows - 1)) * D;
 #pragma unroll
@@ -122,7 +131,7 @@ __global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split s
   };
   u32x4_t kr[2][KL];
   uint32_t vr[8][VD];
-  auto load = [&](int s, const int (&e)[2], u32x4_t(&kd)[2][KL], uint32_t(&vd)[8][VD]) {
+  auto load = [&](int s, const int (&e)[2]) {
     const int k0 = begin + s * kStep;
     const uint8_t *kp[2], *vp[2];
 #pragma unroll
@@ -137,21 +146,21 @@ __global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split s
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < KL; ++i) kd[t][i] = *(gu32x4p)(p + t * 4 * row_bytes + i * 64);
+      for (int i = 0; i < KL; ++i) kr[t][i] = load_once((gu32x4p)(p + t * 4 * row_bytes + i * 64));
     const uint8_t* v = (q >> 1 ? vp[1] : vp[0]) + ((k0 + 8 * q) & in) * row_bytes + r * (NB * ES);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (VD == 4) {
-        const u32x4_t w = *(gu32x4p)(v + i * row_bytes);
+        const u32x4_t w = load_once((gu32x4p)(v + i * row_bytes));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) vd[i][j] = w[j];
+        for (int j = 0; j < 4; ++j) vr[i][j] = w[j];
       } else if constexpr (VD == 2) {
         typedef const __attribute__((address_space(1))) u32x2_t* gu32x2p;
-        const u32x2_t w = *(gu32x2p)(v + i * row_bytes);
-        vd[i][0] = w[0], vd[i][1] = w[1];
+        const u32x2_t w = load_once((gu32x2p)(v + i * row_bytes));
+        vr[i][0] = w[0], vr[i][1] = w[1];
       } else {
         typedef const __attribute__((address_space(1))) uint32_t* gu32p;
-        vd[i][0] = *(gu32p)(v + i * row_bytes);
+        vr[i][0] = load_once((gu32p)(v + i * row_bytes));
       }
     }
   };
@@ -161,11 +170,13 @@ __global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split s
 #pragma unroll
   for (int i = 0; i < NB; ++i) o[i] = at_f32x4{0, 0, 0, 0};
 
+  int e[2] = {0, 0}, ahead[2] = {0, 0};
+  if (mine > 0) pages_of(wave, ahead);
   for (int n = 0; n < mine; ++n) {
-    const int s = wave + 4 * n;
-    int e[2];
-    pages_of(s, e);
-    load(s, e, kr, vr);
+    const int s = wave + kWaves * n;
+    e[0] = ahead[0], e[1] = ahead[1];
+    load(s, e);
+    if (n + 1 < mine) pages_of(s + kWaves, ahead);
     // scores
     at_f32x4 sc[2] = {at_f32x4{0, 0, 0, 0}, at_f32x4{0, 0, 0, 0}};
 #pragma unroll
@@ -245,7 +256,7 @@ __global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split s
     }
   }
 
-  // the four waves' sums, joined in their order
+  // the waves' sums, joined in their order
   sum = sum_xor32(sum_xor16(sum));
   if (r < rows) {
     if (q == 0) stats[wave][r][0] = m, stats[wave][r][1] = sum;
@@ -258,14 +269,14 @@ __global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split s
   __syncthreads();
   const bool whole = at.chunks == 1;
   const float vs = whole && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f;
-  for (int idx = threadIdx.x; idx < rows * (D / 2); idx += 256) {
+  for (int idx = threadIdx.x; idx < rows * (D / 2); idx += 64 * kWaves) {
     const int g = idx / (D / 2), d = idx % (D / 2) * 2;
     float most = stats[0][g][0];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) most = fmaxf(most, stats[w][g][0]);
+    for (int w = 1; w < kWaves; ++w) most = fmaxf(most, stats[w][g][0]);
     float total = 0.0f, y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       const float f = part_weight(stats[w][g][0], most);
       total += f * stats[w][g][1];
       y0 += f * part[w][g][d];
@@ -283,46 +294,55 @@ __global__ void __launch_bounds__(256, 2) attn_decode_kernel(AttnArgs a, Split s
   }
 }
 
-// One workgroup for each sequence and head: the chunks' sums, weighed by their maxima, in a fixed order (eight
-// groups of lanes, every eighth chunk each, then the groups).
+// One workgroup for each sequence and head: the parts' sums, weighed by their maxima, in a fixed order (256 / (D / 4)
+// groups of lanes, every so manyeth part each, then the groups).
 template <int D>
 __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split sp) {
   constexpr int LANES = D / 4, GROUPS = 256 / LANES;
   __shared__ at_f32x4 part[GROUPS][LANES];
-  __shared__ float totals[GROUPS];
+  __shared__ float weights[kTarget + 1], totals[4];
   const int h = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
-  const Place at = find_place<true>(a.lens, a.B, a.keys, sp.heads, sp.target, b);
-  if (at.chunks <= 1) return;
-  const int head = h / sp.G, g = h % sp.G, tile = g / kRows;
-  auto slot = [&](int chunk) {
-    return ((int64_t)(at.first + chunk) * sp.heads + head * sp.tiles + tile) * sp.rows + g % kRows;
+  const Place at = find_place<true>(a.lens, a.B, a.keys, sp.heads, b);
+  const int parts = at.chunks;
+  if (parts <= 1) return;
+  const int head = h / sp.G, g = h % sp.G;
+  auto slot = [&](int i) {
+    return ((int64_t)(at.first + i) * sp.heads + head * sp.tiles + g / kRows) * sp.rows + g % kRows;
   };
-  const float* __restrict__ stats = a.ws + stats_at(sp.units, sp.rows, D);
-  float most = kNegInf;
-  for (int i = threadIdx.x & 63; i < at.chunks; i += 64) most = fmaxf(most, stats[2 * slot(i)]);
+  const float2* __restrict__ stats = (const float2*)(a.ws + stats_at(sp.units, sp.rows, D));
+  float most = kNegInf, mine = kNegInf, sum = 0.0f;
+  for (int i = threadIdx.x & 63; i < parts; i += 64) most = fmaxf(most, stats[slot(i)].x);
+  most = max_xor32(max_xor16(most));
 #pragma unroll
-  for (int x = 1; x < 64; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+  for (int x = 1; x < 16; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+  for (int i = threadIdx.x; i < parts; i += 256) {
+    const float2 v = stats[slot(i)];
+    weights[i] = mine = part_weight(v.x, most);
+    sum += mine * v.y;
+  }
+  sum = sum_xor32(sum_xor16(sum));
+#pragma unroll
+  for (int x = 1; x < 16; x *= 2) sum += __shfl_xor(sum, x);
+  if ((threadIdx.x & 63) == 0) totals[threadIdx.x >> 6] = sum;
+  __syncthreads();
   const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
   at_f32x4 y{0, 0, 0, 0};
-  float total = 0.0f;
-  for (int i = group; i < at.chunks; i += GROUPS) {
-    const int64_t s = slot(i);
-    const float f = part_weight(stats[2 * s], most);
-    total += f * stats[2 * s + 1];
-    const at_f32x4 v = *(const at_f32x4*)(a.ws + s * D + 4 * l);
+#pragma unroll 4
+  for (int i = group; i < parts; i += GROUPS) {
+    const at_f32x4 v = *(const at_f32x4*)(a.ws + slot(i) * D + 4 * l);
+    const float f = weights[i];
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] += f * v[j];
   }
   part[group][l] = y;
-  if (l == 0) totals[group] = total;
   __syncthreads();
   if (group) return;
 #pragma unroll
   for (int i = 1; i < GROUPS; ++i) {
-    total += totals[i];
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] += part[i][l][j];
   }
+  const float total = (totals[0] + totals[1]) + (totals[2] + totals[3]);
   const float inv = total == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / total;
   *(u32x2_t*)(a.out + ((int64_t)b * a.Hq + h) * D + 4 * l) =
       u32x2_t{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
@@ -331,9 +351,10 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split
 template <int D>
 void launch(const AttnArgs& a, const Split& sp, hipStream_t stream) {
   const bool split = may_split(a.keys);
-  const int64_t units = split ? sp.units : (int64_t)a.B * sp.heads;
-  if (a.kv.f8) attn_decode_kernel<D, true><<<(uint32_t)units, 256, 0, stream>>>(a, sp);
-  else attn_decode_kernel<D, false><<<(uint32_t)units, 256, 0, stream>>>(a, sp);
+  const uint32_t units = (uint32_t)(split ? sp.units : (int64_t)a.B * sp.heads);
+  auto* kernel = a.kv.f8 ? (split ? attn_decode_kernel<D, true, true> : attn_decode_kernel<D, true, false>)
+                         : (split ? attn_decode_kernel<D, false, true> : attn_decode_kernel<D, false, false>);
+  kernel<<<units, 64 * kWaves, 0, stream>>>(a, sp);
   if (split) attn_decode_join_kernel<D><<<(uint32_t)(a.B * a.Hq), 256, 0, stream>>>(a, sp);
 }
 

@@ -86,10 +86,25 @@ struct Keys {
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((address_space(3))) s16x4_t* ls16x4p;
 
-// Where 16-byte column c of a key's row lies in LDS, so that neither K's reads (16 bytes of 16 keys at a time)
-// nor V's (32 bytes of four keys) meet in a bank
-template <int D> __device__ __forceinline__ int swizzle_k(int key) { return key & (D / 8 - 1); }
-template <int D> __device__ __forceinline__ int swizzle_v(int key) { return 2 * (key & (D / 16 - 1)); }
+// Column c (16 bytes) of a key's row lies at column c ^ swizzle in LDS.  The 64 banks hold 256 bytes, so that
+// neither K's reads (a column of 16 keys at a time) nor V's (four columns of four keys) meet in one.
+template <int D> __device__ __forceinline__ int swizzle_k(int key) { return D == 128 ? key & 15 : (key >> 1) & 7; }
+template <int D> __device__ __forceinline__ int swizzle_v(int key) { return D == 128 ? 4 * (key & 3) : 4 * ((key >> 1) & 1); }
+
+// A wave's 16 keys straight into LDS at lds, 1 KB a piece (an instruction's offset moves both of its addresses);
+// off[i]: the lane's place in piece i.  As for the loads in ql_mx4.hpp, readers wait, and the wait states are kept here.
+__device__ __forceinline__ void dma_pieces(uint32_t lds, const uint8_t* base, const uint32_t (&off)[4]) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+               "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+               "global_load_lds_dwordx4 %4, %5 offset:3072"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]),
+                  "s"(uniform_ptr(base)) : "memory");
+}
+__device__ __forceinline__ void dma_pieces(uint32_t lds, const uint8_t* base, const uint32_t (&off)[2]) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+               "global_load_lds_dwordx4 %2, %3 offset:1024"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off[0]), "v"(off[1]), "s"(uniform_ptr(base)) : "memory");
+}
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptPlan plan) {
@@ -128,35 +143,32 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   const int shift = a.kv.page_shift;
   const uint32_t in_page = (1u << shift) - 1;
   const uint32_t lds0 = lds_offset(smem);
-  // Entries of a tile's four groups of 16 keys; wave w brings group w.  A group behind the last key takes the last
-  // key's page; entries that are no page read page 0 and are masked (bit g of the result).
+  // Entries of a tile's four groups of 16 keys, lane g that of group g (mod 4), read a tile ahead; wave w brings
+  // group w.  A group behind the last key takes the last key's page; entries that are no page read page 0 and
+  // are masked (bit g of `bad`).
   const int key_last = max(1, min(rt.len, kTileKeys * keys.tiles)) - 1;
+  auto entry = [&](int t) { return row[min(t * kTileKeys + 16 * (lane & 3), key_last) >> shift]; };
   struct Source { const uint8_t *k, *v; int bad; };
-  auto source = [&](int t) {
-    Source s{nullptr, nullptr, 0};
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int key = t * kTileKeys + 16 * g, e = row[min(key, key_last) >> shift];
-      const bool ok = (uint32_t)e < (uint32_t)a.kv.pages;
-      s.bad |= ok ? 0 : 1 << g;
-      if (g == wave) {
-        const int64_t off = ((((int64_t)(ok ? e : 0) * Hkv + head) << shift) + (key & in_page)) * (int64_t)(F8 ? D : 2 * D);
-        s.k = a.kv.k + off, s.v = a.kv.v + off;
-      }
-    }
-    return s;
+  auto source = [&](int t, int e) {
+    const int own = __builtin_amdgcn_readlane(e, wave);
+    const int page = (uint32_t)own < (uint32_t)a.kv.pages ? own : 0;
+    const int64_t off = ((((int64_t)page * Hkv + head) << shift) + ((t * kTileKeys + 16 * wave) & in_page)) * (int64_t)(F8 ? D : 2 * D);
+    return Source{a.kv.k + off, a.kv.v + off, (int)(__ballot((uint32_t)e >= (uint32_t)a.kv.pages) & 15)};
   };
-  // bf16: straight into LDS, 1 KB (4 or 8 keys) an instruction
+  // bf16: straight into LDS, 1 KB (4 or 8 keys) a piece
   constexpr int PIECES = 16 * ROW / 1024, PER = 1024 / ROW;
+  uint32_t k_off[PIECES], v_off[PIECES];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int at = lane / (64 / PER), col = lane % (64 / PER), key = PER * i + at;
+    k_off[i] = at * ROW + (col ^ swizzle_k<D>(key)) * 16;
+    v_off[i] = at * ROW + (col ^ swizzle_v<D>(key)) * 16;
+  }
   auto send = [&](const Source& s, int buf) {
     if constexpr (!F8) {
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int key = PER * i + lane / (64 / PER), col = lane % (64 / PER);
-        const uint32_t to = lds0 + buf * 2 * TILE + wave * 16 * ROW + i * 1024;
-        dma16(to, s.k, key * ROW + ((col ^ swizzle_k<D>(key)) * 16));
-        dma16(to + TILE, s.v, key * ROW + ((col ^ swizzle_v<D>(key)) * 16));
-      }
+      const uint32_t to = lds0 + buf * 2 * TILE + wave * 16 * ROW;
+      dma_pieces(to, s.k, k_off);
+      dma_pieces(to + TILE, s.v, v_off);
     }
   };
   // e4m3: through registers, widened on the way
@@ -210,9 +222,10 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   uint32_t infinities[DT] = {};  // bit e: +inf to o[dt][e], 16 + e: -inf
 
   Source next = {};
-  int bad = 0;
+  int bad = 0, ahead = 0;
   if (t0 < t1) {
-    next = source(t0);
+    next = source(t0, entry(t0));
+    ahead = entry(t0 + 1);
     send(next, 0);
     fetch(next);
     put(0);
@@ -226,9 +239,10 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
     barrier();
     const int bad_now = bad;
     if (t + 1 < t1) {
-      next = source(t + 1);
+      next = source(t + 1, ahead);
       send(next, buf ^ 1);
       fetch(next);
+      ahead = entry(t + 2);
       bad = next.bad;
     }
     // 0 * inf is NaN, also where a weight is 0 because the row does not see the key, and what memory behind the
@@ -284,7 +298,8 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
       }
       const bool masked = key0 + kTileKeys > limit_first || bad_now;
       if (masked) {
-        const int visible = limit - key0 - 4 * j;
+        int visible = limit - key0 - 4 * j;
+        asm volatile("" : "+v"(visible));  // a branch: few tiles need it
 #pragma unroll
         for (int z = 0; z < 2; ++z)
 #pragma unroll

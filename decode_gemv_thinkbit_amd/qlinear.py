@@ -799,32 +799,32 @@ class KvCache:
     v_scale: Optional[torch.Tensor] = None
 
     def __post_init__(self):
-        k, v = self.k, self.v
-        if k.dtype not in _CACHE_TYPES or v.dtype != k.dtype:
+        k, v, shape, device = self.k, self.v, self.k.shape, self.k.device
+        kind = _CACHE_TYPES.get(k.dtype)
+        if kind is None or v.dtype is not k.dtype:
             raise ValueError(f"k and v must be both bfloat16 or both float8_e4m3fn, got {k.dtype} and {v.dtype}")
-        if k.dim() != 4 or v.shape != k.shape or not k.numel():
-            raise ValueError(f"k and v must be [pages, heads, page, D], got {tuple(k.shape)} and {tuple(v.shape)}")
+        if len(shape) != 4 or v.shape != shape or 0 in shape:
+            raise ValueError(f"k and v must be [pages, heads, page, D], got {tuple(shape)} and {tuple(v.shape)}")
         if not (k.is_contiguous() and v.is_contiguous()):
             raise ValueError("k and v must be contiguous")
-        pages, heads, page, D = k.shape
-        if D not in (64, 128):
+        pages, heads, page, D = shape
+        if D != 64 and D != 128:
             raise ValueError(f"heads must have 64 or 128 dims, got {D}")
         if not 16 <= page <= 4096 or page & (page - 1):
             raise ValueError(f"a page must hold 16..4096 tokens, a power of two, got {page}")
-        for s, name in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
-            if k.dtype == torch.bfloat16:
-                if s is not None:
-                    raise ValueError(f"{name}: a bfloat16 cache has no scales")
-            elif s is None or s.dtype != torch.float32 or s.shape != (heads,) or not s.is_contiguous() or \
-                    s.device != k.device:
-                raise ValueError(f"{name} must be float32 [{heads}], contiguous, on the cache's device")
-        if v.device != k.device:
+        if v.device != device:
             raise ValueError("k and v must be on one device")
-        object.__setattr__(self, "shape", (pages, heads, page, D))
-        object.__setattr__(self, "desc", ql_kv_cache(
-            pages, heads, page, D, _CACHE_TYPES[k.dtype], 0, k.data_ptr(), v.data_ptr(),
-            None if self.k_scale is None else self.k_scale.data_ptr(),
-            None if self.v_scale is None else self.v_scale.data_ptr()))
+        scales = self.k_scale, self.v_scale
+        for s in scales:
+            if k.dtype is torch.bfloat16:
+                if s is not None:
+                    raise ValueError("a bfloat16 cache has no scales")
+            elif s is None or s.dtype is not torch.float32 or s.shape != (heads,) or not s.is_contiguous() or \
+                    s.device != device:
+                raise ValueError(f"k_scale and v_scale must be float32 [{heads}], contiguous, on the cache's device")
+        desc = ql_kv_cache(pages, heads, page, D, kind, 0, k.data_ptr(), v.data_ptr(),
+                           *(s if s is None else s.data_ptr() for s in scales))
+        self.__dict__.update(shape=(pages, heads, page, D), device=device, desc=ctypes.byref(desc))
 
     @property
     def nbytes(self) -> int:
@@ -847,8 +847,8 @@ class Rope:
         f = self.freqs
         if f.dtype != torch.float32 or f.dim() != 1 or not f.numel() or not f.is_contiguous():
             raise ValueError("freqs must be float32 [pairs], contiguous")
-        object.__setattr__(self, "desc", ql_rope(f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0,
-                                                 float(self.factor), 0))
+        self.__dict__["desc"] = ctypes.byref(ql_rope(f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0,
+                                                     float(self.factor), 0))
 
 
 def rope_frequencies(dims: int, base: float = 10000.0, stretch: float = 1.0, original: Optional[int] = None,
@@ -876,28 +876,38 @@ def rope_frequencies(dims: int, base: float = 10000.0, stretch: float = 1.0, ori
     return torch.from_numpy(f.astype(np.float32)), 0.1 * float(np.log(stretch)) + 1.0
 
 
-def _int32(t: torch.Tensor, shape: tuple, device: torch.device, name: str):
-    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be int32 {list(shape)}, contiguous, on {device}, got {t.dtype} {list(t.shape)}")
+def _int32(t: torch.Tensor, n: int, device: torch.device, name: str) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be int32 [{n}], contiguous, on {device}, got {t.dtype} {list(t.shape)}")
     return t.data_ptr()
 
 
 def _cache(cache: KvCache, device: torch.device):
+    """The device's cache's (pages, heads, page, D)."""
     if not isinstance(cache, KvCache):
         raise ValueError("cache must be a KvCache")
-    if cache.k.device != device:
-        raise ValueError("the cache must be on the device of the other operands, a CUDA (HIP) device")
-    return ctypes.byref(cache.desc)
+    if cache.device != device or device.type != "cuda":
+        raise ValueError("the operands and the cache must be on one CUDA (HIP) device")
+    return cache.shape
 
 
-def _heads(x: torch.Tensor, D: int, name: str) -> int:
-    """The heads of x [T, heads, D] or [T, heads * D], rows at any distance."""
-    if x.dim() == 3:
-        if x.shape[2] == D and x.stride(2) == 1 and (x.stride(1) == D or x.shape[1] == 1):
-            return x.shape[1]
-    elif x.dim() == 2 and x.shape[1] % D == 0 and x.stride(1) == 1:
-        return x.shape[1] // D
-    raise ValueError(f"{name} must be [T, heads, {D}] or [T, heads * {D}] with contiguous rows, got {tuple(x.shape)}")
+def _rows(x: torch.Tensor, D: int, name: str) -> tuple[int, int]:
+    """(heads, values between rows) of x [T, heads, D] or [T, heads * D], rows at any distance."""
+    shape, strides = x.shape, x.stride()
+    if len(shape) == 3:
+        if shape[2] == D and strides[2] == 1 and (strides[1] == D or shape[1] == 1):
+            return shape[1], strides[0]
+    elif len(shape) == 2 and shape[1] % D == 0 and strides[1] == 1:
+        return shape[1] // D, strides[0]
+    raise ValueError(f"{name} must be [T, heads, {D}] or [T, heads * {D}] with contiguous rows, got {tuple(shape)}")
+
+
+def _norm(n: Optional[torch.Tensor], D: int, device: torch.device, name: str):
+    if n is None:
+        return None
+    if n.dtype is not torch.float32 or n.shape != (D,) or not n.is_contiguous() or n.device != device:
+        raise ValueError(f"{name} must be float32 [{D}], contiguous, on {device}")
+    return n.data_ptr()
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -907,47 +917,37 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     q [T, Hq, D] or [T, Hq * D], k and v alike with the cache's heads (fp32, bf16 or fp16, all of one type; rows
     may be parts of wider ones); positions, slots int32 [T], a slot outside the cache (-1) is not written, and no
     slot may appear twice.  q_norm, k_norm (fp32 [D]): x * norm / sqrt(mean x^2 + eps) over each head first."""
-    device = q.device
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA (HIP) tensor")
-    desc = _cache(cache, device)
-    if q.dtype not in _DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError(f"q, k and v must be all float32, bfloat16 or float16, got {q.dtype}, {k.dtype}, {v.dtype}")
-    _, Hkv, _, D = cache.shape
-    Hq = _heads(q, D, "q")
+    device, dtype = q.device, q.dtype
+    _, Hkv, _, D = _cache(cache, device)
+    if dtype not in _DTYPES or k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError(f"q, k and v must be all float32, bfloat16 or float16, got {dtype}, {k.dtype}, {v.dtype}")
     T = q.shape[0]
-    if _heads(k, D, "k") != Hkv or _heads(v, D, "v") != Hkv or k.shape[0] != T or v.shape[0] != T or \
-            k.device != device or v.device != device:
+    (Hq, q_stride), (k_heads, k_stride), (v_heads, v_stride) = _rows(q, D, "q"), _rows(k, D, "k"), _rows(v, D, "v")
+    if k_heads != Hkv or v_heads != Hkv or k.shape[0] != T or v.shape[0] != T or k.device != device or \
+            v.device != device:
         raise ValueError(f"k and v must be [{T}, {Hkv}, {D}] on {device}")
     if not isinstance(rope, Rope) or rope.freqs.device != device:
         raise ValueError(f"rope must be a Rope with its frequencies on {device}")
-    norms = [None, None]
-    for i, n in enumerate((q_norm, k_norm)):
-        if n is not None:
-            if n.dtype != torch.float32 or n.shape != (D,) or n.device != device or not n.is_contiguous():
-                raise ValueError(f"{'qk'[i]}_norm must be float32 [{D}] on {device}")
-            norms[i] = n.data_ptr()
-    pos, slot = _int32(positions, (T,), device, "positions"), _int32(slots, (T,), device, "slots")
     out = _result(out, q.shape, torch.bfloat16, device)
-    _launch("rope_append", lib().qlinear_rope_append, device, T, Hq, _DTYPES[q.dtype], q.data_ptr(), q.stride(0),
-            k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), pos, slot, ctypes.byref(rope.desc), norms[0], norms[1],
-            eps, desc, out.data_ptr())
+    _launch("rope_append", lib().qlinear_rope_append, device, T, Hq, _DTYPES[dtype], q.data_ptr(), q_stride,
+            k.data_ptr(), k_stride, v.data_ptr(), v_stride, _int32(positions, T, device, "positions"),
+            _int32(slots, T, device, "slots"), rope.desc, _norm(q_norm, D, device, "q_norm"),
+            _norm(k_norm, D, device, "k_norm"), eps, cache.desc, out.data_ptr())
     return out
 
 
 def _attention(q, cache, table, lens, scale):
-    """Checks both attentions make: (device, cache's descriptor, rows, Hq, sequences, pages of a row, scale)."""
+    """What both attentions check: (device, cache's heads, page, D, rows, Hq, sequences, pages of a row, scale)."""
     device = q.device
-    _dev(q, torch.bfloat16, "q")
-    desc = _cache(cache, device)
-    D = cache.shape[3]
-    Hq = _heads(q, D, "q")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1 and table.shape[1] != 1 or \
-            table.device != device:
+    _, Hkv, page, D = _cache(cache, device)
+    if q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise ValueError(f"q must be torch.bfloat16, contiguous, got {q.dtype}")
+    Hq, _ = _rows(q, D, "q")
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.device != device or \
+            (table.stride(1) != 1 and table.shape[1] != 1):
         raise ValueError(f"table must be int32 [B, pages of a sequence] on {device}, its rows contiguous")
     B, most = table.shape
-    _int32(lens, (B,), device, "lens")
-    return device, desc, q.shape[0], Hq, B, most, D ** -0.5 if scale is None else float(scale)
+    return device, Hkv, page, D, q.shape[0], Hq, B, most, D ** -0.5 if scale is None else scale
 
 
 def attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lens: torch.Tensor, scale: Optional[float] = None,
@@ -956,15 +956,14 @@ def attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lens: torc
     lens[b] tokens (int32 [B]; 0: the result is 0) in the pages that table[b] (int32 [B, pages]) names in order.
     Hq is a multiple of the cache's heads; entries that are no page stand for tokens that are not seen.
     scale: of the scores, D ** -0.5 unless given."""
-    device, desc, rows, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
+    device, Hkv, page, D, rows, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
     if rows != B:
         raise ValueError(f"q has {rows} rows, the table {B}")
     out = _result(out, q.shape, torch.bfloat16, device)
-    _, Hkv, page, D = cache.shape
     need = _workspace_bytes("attn_decode", device, B, Hq, Hkv, D, most * page)
-    workspace = _scratch(workspace, need, device) if need else None
-    _launch("attn_decode", lib().qlinear_attn_decode, device, desc, B, Hq, q.data_ptr(), table.data_ptr(),
-            table.stride(0), most, lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr() if need else None, need)
+    workspace = _scratch(workspace, need, device).data_ptr() if need else None
+    _launch("attn_decode", lib().qlinear_attn_decode, device, cache.desc, B, Hq, q.data_ptr(), table.data_ptr(),
+            table.stride(0), most, _int32(lens, B, device, "lens"), scale, out.data_ptr(), workspace, need)
     return out
 
 
@@ -975,15 +974,13 @@ def attn_prompt(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, table: to
     of q [T, Hq, D] or [T, Hq * D] bf16 (starts int32 [B + 1], ascending) are the last tokens of sequence b, whose
     lens[b] tokens (those rows' included) are in the pages of table[b].  Row i of n sees tokens 0 .. lens[b] - n + i;
     one that sees none gives 0; rows that belong to no sequence are not written.  The rest as for attn_decode."""
-    device, desc, T, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
-    _int32(starts, (B + 1,), device, "starts")
+    device, Hkv, page, D, T, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
     out = _result(out, q.shape, torch.bfloat16, device)
-    _, Hkv, page, D = cache.shape
     need = _workspace_bytes("attn_prompt", device, T, B, Hq, Hkv, D, most * page)
-    workspace = _scratch(workspace, need, device) if need else None
-    _launch("attn_prompt", lib().qlinear_attn_prompt, device, desc, T, B, Hq, q.data_ptr(), starts.data_ptr(),
-            table.data_ptr(), table.stride(0), most, lens.data_ptr(), scale, out.data_ptr(),
-            workspace.data_ptr() if need else None, need)
+    workspace = _scratch(workspace, need, device).data_ptr() if need else None
+    _launch("attn_prompt", lib().qlinear_attn_prompt, device, cache.desc, T, B, Hq, q.data_ptr(),
+            _int32(starts, B + 1, device, "starts"), table.data_ptr(), table.stride(0), most,
+            _int32(lens, B, device, "lens"), scale, out.data_ptr(), workspace, need)
     return out
 
 
