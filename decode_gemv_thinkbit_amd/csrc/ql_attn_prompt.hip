@@ -23,20 +23,24 @@ namespace ql {
 namespace {
 
 constexpr int kTileRows = 128, kTileKeys = 64;
-constexpr int kMinSplit = 8;     // tiles of keys of a part at least
+constexpr int kMaxSplits = 32;
 constexpr float kLag = 8.0f;     // how far (in powers of two) scores may pass the maximum in use
 
 struct PromptPlan {
-  int G, splits;
-  int64_t tiles;  // row tiles of a kv head at most
+  int G, splits, least;  // least: tiles of keys of a part at least
+  int64_t tiles;         // row tiles of a kv head at most
 };
+// Two workgroups fit a CU: where the rows do not make that many, the keys are split.  A part costs its rows' sums
+// in fp32 written and read, so parts are long but where rows are few (32 over 8 heads of 128: 512 tokens take 16.8 us
+// in one part, 20.7 in two of 256 keys; 64 tokens behind 4000 29.6 us in parts of 128 keys, 24.0 of 256,
+// 24.9 of 512; 4 behind 1000 17.1 in parts of 512, 13.0 of 256).
 PromptPlan plan_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t keys) {
   PromptPlan p;
   p.G = (int)(Hq / Hkv);
   p.tiles = T * p.G / kTileRows + B;
-  // Two workgroups fit a CU: where the rows do not make that many, the keys are split.
+  p.least = T * p.G <= 2 * kTileRows ? 4 : 16;
   const int64_t blocks = (T * p.G + kTileRows - 1) / kTileRows * Hkv;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({768 / blocks, keys / (kMinSplit * kTileKeys), 32}));
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / blocks, keys / (p.least * kTileKeys), kMaxSplits}));
   return p;
 }
 
@@ -44,15 +48,19 @@ struct RowTile {
   int b, first, n, len, row0;  // sequence, its first row of q, queries, cached tokens, first (query, head) of the tile
 };
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
+// Number `want` of all sequences' tiles, a sequence's last tile, which sees the most keys, first.  (The longest
+// tiles of all sequences first were slower, though better balanced: 13 packed sequences of 47 .. 1184 tokens 101 us
+// against 95; workgroups that run together then share no keys.)
 __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want) {
   const int lane = threadIdx.x & 63;
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     const int b = b0 + lane;
-    int first = 0, n = 0;
+    int first = 0, n = 0, len = 0;
     if (b < a.B) {
       first = clamp_to(a.starts[b], 0, a.T);
       n = clamp_to(a.starts[b + 1], first, a.T) - first;
+      len = clamp_to(a.lens[b], 0, a.keys);
     }
     const uint32_t upto = before + scan_lanes((uint32_t)(n * G + kTileRows - 1) / kTileRows);
     const uint64_t here = __ballot((uint32_t)want < upto);
@@ -62,8 +70,7 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want)
       t.b = b0 + l;
       t.first = __builtin_amdgcn_readlane(first, l);
       t.n = __builtin_amdgcn_readlane(n, l);
-      t.len = clamp_to(a.lens[t.b], 0, a.keys);
-      // the longest rows first
+      t.len = __builtin_amdgcn_readlane(len, l);
       t.row0 = (__builtin_amdgcn_readlane((int)upto, l) - 1 - want) * kTileRows;
       return t;
     }
@@ -75,10 +82,10 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want)
 // the tiles of keys of a row tile, and of one of its parts
 struct Keys {
   int tiles, per;
-  __device__ __forceinline__ Keys(const RowTile& t, int G, int splits) {
-    const int last = min((t.row0 + kTileRows - 1) / G, t.n - 1);
+  __device__ __forceinline__ Keys(const RowTile& t, const PromptPlan& p) {
+    const int last = min((t.row0 + kTileRows - 1) / p.G, t.n - 1);
     tiles = (max(t.len - t.n + last + 1, 0) + kTileKeys - 1) / kTileKeys;
-    per = max((tiles + splits - 1) / splits, kMinSplit);
+    per = max((tiles + p.splits - 1) / p.splits, p.least);
   }
   __device__ __forceinline__ int parts() const { return max(1, (tiles + per - 1) / per); }
 };
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   const int split = blockIdx.x % plan.splits, unit = blockIdx.x / plan.splits, head = unit % Hkv;
   const RowTile rt = find_tile(a, G, unit / Hkv);
   if (rt.b < 0) return;
-  const Keys keys(rt, G, plan.splits);
+  const Keys keys(rt, plan);
   const int t0 = split * keys.per, t1 = min(keys.tiles, t0 + keys.per);
   if (split && t0 >= t1) return;
   const bool whole = keys.parts() == 1;
@@ -126,14 +133,15 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   const int rows = rt.n * G - rt.row0;  // those of the tile, or more
   const int base_pos = rt.len - rt.n + 1;
   const int mine = min(wave * 32 + r, rows - 1) + rt.row0;
-  const int limit = base_pos + mine / G;  // keys that this row sees
+  const int query = mine / G, in_group = mine - query * G;
+  const int limit = base_pos + query;  // keys that this row sees
   const int limit_first = base_pos + min(rt.row0 + wave * 32, rt.n * G - 1) / G;
   const int limit_tile = base_pos + rt.row0 / G;
   const int limit_last = base_pos + min(rt.row0 + wave * 32 + 31, rt.n * G - 1) / G;
 
   u32x4_t qf[DK];
   {
-    const uint16_t* p = a.q + ((int64_t)(rt.first + mine / G) * a.Hq + (int64_t)head * G + mine % G) * D + 8 * j;
+    const uint16_t* p = a.q + ((int64_t)(rt.first + query) * a.Hq + (int64_t)head * G + in_group) * D + 8 * j;
 #pragma unroll
     for (int i = 0; i < DK; ++i) qf[i] = *(gu32x4p)(p + 16 * i);
   }
@@ -224,13 +232,17 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   Source next = {};
   int bad = 0, ahead = 0;
   if (t0 < t1) {
-    next = source(t0, entry(t0));
+    const int now = entry(t0);
     ahead = entry(t0 + 1);
+    next = source(t0, now);
     send(next, 0);
     fetch(next);
     put(0);
     bad = next.bad;
   }
+  // q has come here, not in the loop: there a wait for it would be one for the loads into LDS too
+#pragma unroll
+  for (int i = 0; i < DK; ++i) asm volatile("" : "+v"(qf[i]));
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1, key0 = t * kTileKeys;
     const uint8_t *kt = smem + buf * 2 * TILE, *vt = kt + TILE;
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
     }
   if (whole) {
     const float inv = sum == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / sum;
-    uint16_t* out = a.out + ((int64_t)(rt.first + mine / G) * a.Hq + (int64_t)head * G + mine % G) * D;
+    uint16_t* out = a.out + ((int64_t)(rt.first + query) * a.Hq + (int64_t)head * G + in_group) * D;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -394,25 +406,43 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, Promp
   const int Hkv = a.kv.heads, G = plan.G, unit = blockIdx.x, head = unit % Hkv;
   const RowTile rt = find_tile(a, G, unit / Hkv);
   if (rt.b < 0) return;
-  const Keys keys(rt, G, plan.splits);
+  const Keys keys(rt, plan);
   const int parts = keys.parts(), l = threadIdx.x % LANES, row = blockIdx.y * ROWS + threadIdx.x / LANES;
   if (parts == 1 || row >= rt.n * G - rt.row0) return;
   const float* __restrict__ stats = a.ws + plan.tiles * Hkv * plan.splits * kTileRows * D;
   auto slot = [&](int s) { return ((int64_t)unit * plan.splits + s) * kTileRows + row; };
-  float most = kNegInf;
-  for (int s = 0; s < parts; ++s) most = fmaxf(most, stats[2 * slot(s)]);
-  at_f32x4 y{0, 0, 0, 0};
-  float total = 0.0f;
-  for (int s = 0; s < parts; ++s) {
-    const float f = part_weight(stats[2 * slot(s)], most);
-    total += f * stats[2 * slot(s) + 1];
-    const at_f32x4 v = *(const at_f32x4*)(a.ws + slot(s) * D + 4 * l);
+  // lane l of a row's has the maxima and sums of parts l, LANES + l, ..., then every lane those of all
+  float most = kNegInf, total = 0.0f, mine_m[kMaxSplits / LANES], mine_w[kMaxSplits / LANES];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] += f * v[i];
+  for (int i = 0; i < kMaxSplits / LANES; ++i) {
+    const float2 v = i * LANES + l < parts ? *(const float2*)(stats + 2 * slot(i * LANES + l)) : make_float2(kNegInf, 0.0f);
+    mine_m[i] = v.x, mine_w[i] = v.y;
+    most = fmaxf(most, v.x);
+  }
+#pragma unroll
+  for (int x = 1; x < LANES; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / LANES; ++i) {
+    const float f = i * LANES + l < parts ? part_weight(mine_m[i], most) : 0.0f;
+    total += f * mine_w[i];
+    mine_w[i] = f;
+  }
+#pragma unroll
+  for (int x = 1; x < LANES; x *= 2) total += __shfl_xor(total, x);
+  at_f32x4 y{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / LANES; ++i) {
+#pragma unroll 8
+    for (int s = i * LANES; s < min(parts, (i + 1) * LANES); ++s) {
+      const at_f32x4 v = *(const at_f32x4*)(a.ws + slot(s) * D + 4 * l);
+      const float f = __shfl(mine_w[i], s % LANES, LANES);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] += f * v[e];
+    }
   }
   const float inv = total == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / total;
-  const int mine = rt.row0 + row;
-  *(u32x2_t*)(a.out + ((int64_t)(rt.first + mine / G) * a.Hq + (int64_t)head * G + mine % G) * D + 4 * l) =
+  const int query = (rt.row0 + row) / G, in_group = rt.row0 + row - query * G;
+  *(u32x2_t*)(a.out + ((int64_t)(rt.first + query) * a.Hq + (int64_t)head * G + in_group) * D + 4 * l) =
       u32x2_t{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
 }
 
