@@ -29,39 +29,53 @@ constexpr int kRows = 16;                    // heads a workgroup takes at most
 
 // Work is cut on the device, where the lengths are: chunks of equal length C over all sequences, C the least
 // (a multiple of kChunkStep) for which the grid, kTarget + one for each sequence and head, holds them all.
-// Every wave finds its place by itself, 64 sequences at a time.
+// Every wave finds its place by itself, 256 sequences at a time.
 struct Place {
   int b, len, chunk, chunks, first, size;  // first: the number of b's first chunk; size: keys of a chunk
 };
 __device__ __forceinline__ int clamp_len(int len, int keys) { return len < 0 ? 0 : len > keys ? keys : len; }
 
-template <bool BY_SEQUENCE>  // sequence `want`, or the one that has chunk number `want` (b < 0: none)
+// The sequence that has chunk number `want` (b < 0: none)
 __device__ __forceinline__ Place find_place(const int32_t* __restrict__ lens, int B, int keys, int heads, int want) {
   const int lane = threadIdx.x & 63;
-  auto length = [&](int b) { return b < B ? clamp_len(lens[b], keys) : -1; };
-  auto steps = [&](int len) { return len < 0 ? 0u : max(1u, ((uint32_t)len + kChunkStep - 1) / kChunkStep); };
-  const int len0 = length(lane);
-  uint32_t total = last_lane(scan_lanes(steps(len0)));
-  for (int b0 = 64; b0 < B; b0 += 64) total += last_lane(scan_lanes(steps(length(b0 + lane))));
+  int len[4];  // of sequences b0 + 64 i + lane; -1: none
+  auto read = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = b0 + 64 * i + lane;
+      len[i] = b < B ? lens[b] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) len[i] = b0 + 64 * i + lane < B ? clamp_len(len[i], keys) : -1;
+  };
+  auto steps = [](int n) { return n < 0 ? 0u : max(1u, ((uint32_t)n + kChunkStep - 1) / kChunkStep); };
+  uint32_t total = 0;
+  for (int b0 = (B - 1) & ~255; b0 >= 0; b0 -= 256) {  // ends with the first ones read
+    read(b0);
+    total += last_lane(scan_lanes(steps(len[0]) + steps(len[1]) + steps(len[2]) + steps(len[3])));
+  }
   const uint32_t c = (uint32_t)(((uint64_t)total * (uint32_t)heads + kTarget - 1) / kTarget);
   uint32_t before = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    const int len = b0 ? length(b0 + lane) : len0;
-    const uint32_t n = (steps(len) + c - 1) / c;
-    const uint32_t upto = before + scan_lanes(n);
-    const uint64_t here = __ballot(BY_SEQUENCE ? b0 + lane == want : (uint32_t)want < upto);
-    if (here) {
-      const int l = __builtin_ctzll(here);
-      Place p;
-      p.b = b0 + l;
-      p.len = __builtin_amdgcn_readlane(len, l);
-      p.chunks = __builtin_amdgcn_readlane((int)n, l);
-      p.first = __builtin_amdgcn_readlane((int)upto, l) - p.chunks;
-      p.chunk = BY_SEQUENCE ? 0 : want - p.first;
-      p.size = (int)c * kChunkStep;
-      return p;
+  for (int b0 = 0; b0 < B; b0 += 256) {
+    if (b0) read(b0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (b0 + 64 * i >= B) break;
+      const uint32_t n = (steps(len[i]) + c - 1) / c, upto = before + scan_lanes(n);
+      const uint64_t here = __ballot((uint32_t)want < upto);
+      if (here) {
+        const int l = __builtin_ctzll(here);
+        Place p;
+        p.b = b0 + 64 * i + l;
+        p.len = __builtin_amdgcn_readlane(len[i], l);
+        p.chunks = __builtin_amdgcn_readlane((int)n, l);
+        p.first = __builtin_amdgcn_readlane((int)upto, l) - p.chunks;
+        p.chunk = want - p.first;
+        p.size = (int)c * kChunkStep;
+        return p;
+      }
+      before = last_lane(upto);
     }
-    before = last_lane(upto);
   }
   return Place{-1, 0, 0, 0, 0, 0};
 }
@@ -79,8 +93,10 @@ Split split_of(int64_t B, int64_t Hq, int64_t Hkv) {
 }
 bool may_split(int64_t keys) { return keys > kWhole; }
 
-// Partial results: [unit][row][D] sums of exp2(s - m) v, then [unit][row][2]: m, sum
-__device__ __forceinline__ int64_t stats_at(int64_t units, int rows, int D) { return units * rows * D; }
+// The workspace: [unit][row][D] sums of exp2(s - m) v, [unit][row][2] m and sum; then, for the joining kernel, the
+// keys of a chunk and every sequence's first chunk (where it has more than one).
+__host__ __device__ inline int64_t stats_at(const Split& sp, int D) { return sp.units * sp.rows * D; }
+__host__ __device__ inline int64_t plan_at(const Split& sp, int D) { return sp.units * sp.rows * (D + 2); }
 
 template <int D, bool F8, bool SPLIT>
 __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a, Split sp) {
@@ -96,7 +112,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
   const int unit = blockIdx.x, hk = unit % sp.heads, head = hk / sp.tiles, tile = hk % sp.tiles;
   Place at;
   if constexpr (SPLIT) {
-    at = find_place<false>(a.lens, a.B, a.keys, sp.heads, unit / sp.heads);
+    at = find_place(a.lens, a.B, a.keys, sp.heads, unit / sp.heads);
     if (at.b < 0) return;
   } else {
     const int b = unit / sp.heads, len = clamp_len(a.lens[b], a.keys);
@@ -268,6 +284,11 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
   }
   __syncthreads();
   const bool whole = at.chunks == 1;
+  if (SPLIT && threadIdx.x == 0 && hk == 0 && at.chunk == 0) {
+    int32_t* plan = (int32_t*)(a.ws + plan_at(sp, D));
+    if (at.first == 0) plan[0] = at.size;
+    plan[1 + at.b] = at.first;
+  }
   const float vs = whole && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f;
   for (int idx = threadIdx.x; idx < rows * (D / 2); idx += 64 * kWaves) {
     const int g = idx / (D / 2), d = idx % (D / 2) * 2;
@@ -289,7 +310,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
     } else {
       float* out = a.ws + ((int64_t)unit * sp.rows + g) * D + d;
       *(float2*)out = make_float2(y0, y1);
-      if (d == 0) *(float2*)(a.ws + stats_at(sp.units, sp.rows, D) + ((int64_t)unit * sp.rows + g) * 2) = make_float2(most, total);
+      if (d == 0) *(float2*)(a.ws + stats_at(sp, D) + ((int64_t)unit * sp.rows + g) * 2) = make_float2(most, total);
     }
   }
 }
@@ -302,14 +323,15 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split
   __shared__ at_f32x4 part[GROUPS][LANES];
   __shared__ float weights[kTarget + 1], totals[4];
   const int h = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
-  const Place at = find_place<true>(a.lens, a.B, a.keys, sp.heads, b);
-  const int parts = at.chunks;
+  const int32_t* plan = (const int32_t*)(a.ws + plan_at(sp, D));
+  const int size = plan[0], first = plan[1 + b], len = clamp_len(a.lens[b], a.keys);
+  const int parts = (int)(((uint32_t)len + (uint32_t)size - 1) / (uint32_t)size);
   if (parts <= 1) return;
   const int head = h / sp.G, g = h % sp.G;
   auto slot = [&](int i) {
-    return ((int64_t)(at.first + i) * sp.heads + head * sp.tiles + g / kRows) * sp.rows + g % kRows;
+    return ((int64_t)(first + i) * sp.heads + head * sp.tiles + g / kRows) * sp.rows + g % kRows;
   };
-  const float2* __restrict__ stats = (const float2*)(a.ws + stats_at(sp.units, sp.rows, D));
+  const float2* __restrict__ stats = (const float2*)(a.ws + stats_at(sp, D));
   float most = kNegInf, mine = kNegInf, sum = 0.0f;
   for (int i = threadIdx.x & 63; i < parts; i += 64) most = fmaxf(most, stats[slot(i)].x);
   most = max_xor32(max_xor16(most));
@@ -362,7 +384,7 @@ void launch(const AttnArgs& a, const Split& sp, hipStream_t stream) {
 
 size_t attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys) {
   const Split sp = split_of(B, Hq, Hkv);
-  return may_split(keys) ? (size_t)(sp.units * sp.rows * (D + 2)) * sizeof(float) : 0;
+  return may_split(keys) ? (size_t)(plan_at(sp, (int)D) + 1 + B) * sizeof(float) : 0;
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t stream) {
