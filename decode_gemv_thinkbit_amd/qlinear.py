@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -789,21 +790,27 @@ def mx4_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Mx4
 
 
 # ---------------------------------------------------------------- rotary positions and attention
-@dataclass(frozen=True, eq=False)
+_CACHE_TYPES = {torch.bfloat16: 1, torch.float8_e4m3fn: 3}  # ql_dtype
+_pack_cache = struct.Struct("@6i4P").pack  # ql_kv_cache; made in a fifth of the time of a ctypes.Structure
+_pack_rope = struct.Struct("@P2ifi").pack  # ql_rope
+
+
+@dataclass(frozen=True, eq=False, init=False)
 class KvCache:
     """A paged key-value cache: k, v [pages, heads, page, D], bf16, or float8_e4m3fn with one scale per head (a
     stored x stands for x * scale).  Slot number i is place i % page of page i // page."""
     k: torch.Tensor
     v: torch.Tensor
-    k_scale: Optional[torch.Tensor] = None  # fp32 [heads], positive; e4m3 only
-    v_scale: Optional[torch.Tensor] = None
+    k_scale: Optional[torch.Tensor]  # fp32 [heads], positive; e4m3 only
+    v_scale: Optional[torch.Tensor]
 
-    def __post_init__(self):
-        k, v, shape, device = self.k, self.v, self.k.shape, self.k.device
-        kind = _CACHE_TYPES.get(k.dtype)
-        if kind is None or v.dtype is not k.dtype:
-            raise ValueError(f"k and v must be both bfloat16 or both float8_e4m3fn, got {k.dtype} and {v.dtype}")
-        if len(shape) != 4 or v.shape != shape or 0 in shape:
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        shape, dtype, device = k.shape, k.dtype, k.device
+        kind = _CACHE_TYPES.get(dtype)
+        if kind is None or v.dtype is not dtype:
+            raise ValueError(f"k and v must be both bfloat16 or both float8_e4m3fn, got {dtype} and {v.dtype}")
+        if len(shape) != 4 or v.shape != shape or not k.numel():
             raise ValueError(f"k and v must be [pages, heads, page, D], got {tuple(shape)} and {tuple(v.shape)}")
         if not (k.is_contiguous() and v.is_contiguous()):
             raise ValueError("k and v must be contiguous")
@@ -812,19 +819,22 @@ class KvCache:
             raise ValueError(f"heads must have 64 or 128 dims, got {D}")
         if not 16 <= page <= 4096 or page & (page - 1):
             raise ValueError(f"a page must hold 16..4096 tokens, a power of two, got {page}")
+        if pages * page >= 1 << 31 or heads > 4096:
+            raise ValueError(f"fewer than 2^31 tokens and at most 4096 heads, got {tuple(shape)}")
         if v.device != device:
             raise ValueError("k and v must be on one device")
-        scales = self.k_scale, self.v_scale
-        for s in scales:
-            if k.dtype is torch.bfloat16:
-                if s is not None:
-                    raise ValueError("a bfloat16 cache has no scales")
-            elif s is None or s.dtype is not torch.float32 or s.shape != (heads,) or not s.is_contiguous() or \
-                    s.device != device:
-                raise ValueError(f"k_scale and v_scale must be float32 [{heads}], contiguous, on the cache's device")
-        desc = ql_kv_cache(pages, heads, page, D, kind, 0, k.data_ptr(), v.data_ptr(),
-                           *(s if s is None else s.data_ptr() for s in scales))
-        self.__dict__.update(shape=(pages, heads, page, D), device=device, desc=ctypes.byref(desc))
+        if kind == 1:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+            scales = 0, 0
+        else:
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype is not torch.float32 or s.shape != (heads,) or not s.is_contiguous() or \
+                        s.device != device:
+                    raise ValueError(f"k_scale and v_scale must be float32 [{heads}], contiguous, on the cache's device")
+            scales = k_scale.data_ptr(), v_scale.data_ptr()
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, shape=(pages, heads, page, D), device=device,
+                             desc=_pack_cache(pages, heads, page, D, kind, 0, k.data_ptr(), v.data_ptr(), *scales))
 
     @property
     def nbytes(self) -> int:
@@ -832,23 +842,20 @@ class KvCache:
         return 2 * self.k.numel() * self.k.element_size()
 
 
-_CACHE_TYPES = {torch.bfloat16: 1, torch.float8_e4m3fn: 3}  # ql_dtype
-
-
-@dataclass(frozen=True, eq=False)
+@dataclass(frozen=True, eq=False, init=False)
 class Rope:
     """Rotary positions of the first 2 * len(freqs) dims of a head: pair p is turned by position * freqs[p] (fp32,
     on the device) and scaled by factor.  Pairs are dims p and p + len(freqs), or (interleaved) 2p and 2p + 1."""
     freqs: torch.Tensor
-    interleaved: bool = False
-    factor: float = 1.0
+    interleaved: bool
+    factor: float
 
-    def __post_init__(self):
-        f = self.freqs
-        if f.dtype != torch.float32 or f.dim() != 1 or not f.numel() or not f.is_contiguous():
+    def __init__(self, freqs: torch.Tensor, interleaved: bool = False, factor: float = 1.0):
+        shape = freqs.shape
+        if freqs.dtype is not torch.float32 or len(shape) != 1 or not shape[0] or not freqs.is_contiguous():
             raise ValueError("freqs must be float32 [pairs], contiguous")
-        self.__dict__["desc"] = ctypes.byref(ql_rope(f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0,
-                                                     float(self.factor), 0))
+        self.__dict__.update(freqs=freqs, interleaved=interleaved, factor=factor, device=freqs.device,
+                             desc=_pack_rope(freqs.data_ptr(), 2 * shape[0], 1 if interleaved else 0, factor, 0))
 
 
 def rope_frequencies(dims: int, base: float = 10000.0, stretch: float = 1.0, original: Optional[int] = None,
@@ -891,14 +898,18 @@ def _cache(cache: KvCache, device: torch.device):
     return cache.shape
 
 
-def _rows(x: torch.Tensor, D: int, name: str) -> tuple[int, int]:
-    """(heads, values between rows) of x [T, heads, D] or [T, heads * D], rows at any distance."""
+def _rows(x: torch.Tensor, D: int, name: str) -> tuple[int, int, int]:
+    """(T, heads, values between rows) of x [T, heads, D] or [T, heads * D], rows at any distance."""
     shape, strides = x.shape, x.stride()
     if len(shape) == 3:
-        if shape[2] == D and strides[2] == 1 and (strides[1] == D or shape[1] == 1):
-            return shape[1], strides[0]
-    elif len(shape) == 2 and shape[1] % D == 0 and strides[1] == 1:
-        return shape[1] // D, strides[0]
+        T, heads, dims = shape
+        step, of_head, of_dim = strides
+        if dims == D and of_dim == 1 and (of_head == D or heads == 1):
+            return T, heads, step
+    elif len(shape) == 2:
+        T, width = shape
+        if width % D == 0 and strides[1] == 1:
+            return T, width // D, strides[0]
     raise ValueError(f"{name} must be [T, heads, {D}] or [T, heads * {D}] with contiguous rows, got {tuple(shape)}")
 
 
@@ -919,20 +930,20 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     slot may appear twice.  q_norm, k_norm (fp32 [D]): x * norm / sqrt(mean x^2 + eps) over each head first."""
     device, dtype = q.device, q.dtype
     _, Hkv, _, D = _cache(cache, device)
-    if dtype not in _DTYPES or k.dtype is not dtype or v.dtype is not dtype:
+    kind = _DTYPES.get(dtype)
+    if kind is None or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError(f"q, k and v must be all float32, bfloat16 or float16, got {dtype}, {k.dtype}, {v.dtype}")
-    T = q.shape[0]
-    (Hq, q_stride), (k_heads, k_stride), (v_heads, v_stride) = _rows(q, D, "q"), _rows(k, D, "k"), _rows(v, D, "v")
-    if k_heads != Hkv or v_heads != Hkv or k.shape[0] != T or v.shape[0] != T or k.device != device or \
-            v.device != device:
+    T, Hq, q_stride = _rows(q, D, "q")
+    of_k, of_v = _rows(k, D, "k"), _rows(v, D, "v")
+    if of_k[:2] != (T, Hkv) or of_v[:2] != (T, Hkv) or k.device != device or v.device != device:
         raise ValueError(f"k and v must be [{T}, {Hkv}, {D}] on {device}")
-    if not isinstance(rope, Rope) or rope.freqs.device != device:
+    if not isinstance(rope, Rope) or rope.device != device:
         raise ValueError(f"rope must be a Rope with its frequencies on {device}")
     out = _result(out, q.shape, torch.bfloat16, device)
-    _launch("rope_append", lib().qlinear_rope_append, device, T, Hq, _DTYPES[dtype], q.data_ptr(), q_stride,
-            k.data_ptr(), k_stride, v.data_ptr(), v_stride, _int32(positions, T, device, "positions"),
-            _int32(slots, T, device, "slots"), rope.desc, _norm(q_norm, D, device, "q_norm"),
-            _norm(k_norm, D, device, "k_norm"), eps, cache.desc, out.data_ptr())
+    _launch("rope_append", lib().qlinear_rope_append, device, T, Hq, kind, q.data_ptr(), q_stride, k.data_ptr(), of_k[2],
+            v.data_ptr(), of_v[2], _int32(positions, T, device, "positions"), _int32(slots, T, device, "slots"),
+            rope.desc, _norm(q_norm, D, device, "q_norm"), _norm(k_norm, D, device, "k_norm"), eps, cache.desc,
+            out.data_ptr())
     return out
 
 
@@ -942,12 +953,12 @@ def _attention(q, cache, table, lens, scale):
     _, Hkv, page, D = _cache(cache, device)
     if q.dtype is not torch.bfloat16 or not q.is_contiguous():
         raise ValueError(f"q must be torch.bfloat16, contiguous, got {q.dtype}")
-    Hq, _ = _rows(q, D, "q")
-    if table.dtype is not torch.int32 or table.dim() != 2 or table.device != device or \
-            (table.stride(1) != 1 and table.shape[1] != 1):
+    rows, Hq, _ = _rows(q, D, "q")
+    shape = table.shape
+    if table.dtype is not torch.int32 or len(shape) != 2 or table.device != device or \
+            (table.stride(1) != 1 and shape[1] != 1):
         raise ValueError(f"table must be int32 [B, pages of a sequence] on {device}, its rows contiguous")
-    B, most = table.shape
-    return device, Hkv, page, D, q.shape[0], Hq, B, most, D ** -0.5 if scale is None else scale
+    return device, Hkv, page, D, rows, Hq, shape[0], shape[1], D ** -0.5 if scale is None else scale
 
 
 def attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lens: torch.Tensor, scale: Optional[float] = None,

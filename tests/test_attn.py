@@ -105,6 +105,16 @@ def test_null_structs():
                                  FAKE, None) == 1 and "rope" in message()
 
 
+def test_packed_descriptors_are_the_structs():
+    """The binding packs what the header declares."""
+    for pack, of, values in ((ql._pack_cache, ql.ql_kv_cache, (8, 2, 16, 128, 3, 0, FAKE, ODD, BAD, FAKE)),
+                             (ql._pack_rope, ql.ql_rope, (FAKE, 64, 1, 1.25, 0))):
+        raw = pack(*values)
+        assert len(raw) == ctypes.sizeof(of)
+        held = of.from_buffer_copy(raw)
+        assert tuple(getattr(held, f) for f, _ in of._fields_) == values
+
+
 def test_workspace_sizes():
     L = ql.lib()
     assert L.qlinear_attn_decode_workspace_bytes(4, 8, 2, 128, 16) == 0  # one part
