@@ -669,8 +669,8 @@ ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void* q, i
 static ql_status check_attn_sizes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys) {
   QL_TRY(check_heads(Hq, heads, dim));
   if (B < 1 || B > kMaxBlocks) return fail(QL_EINVAL, "1 <= B < 2^24 sequences (B=%lld)", (long long)B);
-  if (keys < 1 || keys >= (int64_t)1 << 31)
-    return fail(QL_EINVAL, "a row of the table holds 1 .. 2^31 - 1 tokens (%lld)", (long long)keys);
+  if (keys < 1 || keys > (int64_t)1 << 30)
+    return fail(QL_EINVAL, "a row of the table holds 1 .. 2^30 tokens (%lld)", (long long)keys);
   return QL_OK;
 }
 

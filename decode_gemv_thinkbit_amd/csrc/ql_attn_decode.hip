@@ -13,6 +13,16 @@
 //  - output of dims x heads (V is the first operand): instruction i's row r is dim (D / 16) r + i, so lane
 //    (q, r) reads of keys 8q .. 8q + 7 the D / 16 dims from (D / 16) r on, whole rows by 16 lanes, and a byte
 //    permute of two keys' dwords makes each operand.  Neither K nor V goes through LDS.
+//
+// Reading the cache bounds.  131072 keys of 8 heads of 128 in bf16 (537 MB) take 80.7 us, 6.6 of the 7.0 TB/s that a
+// pure read reaches, and 87.5 with the join; 64 sequences of 0 .. 8192 keys (253 MB) 48 and 55: a CU fetches at most
+// 35 KB a microsecond, 1.4 times its share, so CUs that got more than others end late.  What that led to:
+//  - keys and values are read past the caches (nontemporal): 105.7 -> 94.0 us for the 131072 keys;
+//  - one step's loads at a time and four workgroups a CU, not two steps' and two: 62 -> 55 us for the 64 sequences,
+//    no difference for long ones (registers: 128, a wave more or less of them decides);
+//  - chunks of equal length, of four waves: equal shares of all sequences' keys, cut anywhere, balance better but wait
+//    at every sequence's end (55.3 us; 33 sequences of heads of 64: 13.7 us against 9.6); full chunks before the
+//    sequences' rests made no difference, nor did shorter or longer chunks (53.5 .. 67 us).
 #include <algorithm>
 
 #include "ql_attn.hpp"
@@ -23,7 +33,9 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                    // keys of a wave's step
 constexpr int kChunkStep = kWaves * kStep;   // a chunk's keys are a multiple: one step of each wave
-constexpr int kWhole = 512;                  // where no sequence can have more keys, each is one chunk
+// Where no sequence can have more keys, each is one chunk and nothing is joined.  Up to 500 keys of one sequence, 32 over 8
+// heads: 8.0 us so and 8.2 in chunks of 128 keys; of 64 sequences 12.1 and 13.9; with 1000 keys 16.6 and 8.2.
+constexpr int kWhole = 512;
 constexpr int kTarget = 1024;                // chunks of a call, about: four workgroups for each CU
 constexpr int kRows = 16;                    // heads a workgroup takes at most
 
@@ -315,11 +327,12 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
   }
 }
 
-// One workgroup for each sequence and head: the parts' sums, weighed by their maxima, in a fixed order (256 / (D / 4)
-// groups of lanes, every so manyeth part each, then the groups).
-template <int D>
+// One workgroup for each sequence, head and slice of its dims: the parts' sums, weighed by their maxima, in a fixed order
+// (GROUPS groups of lanes, every GROUPS-th part each, then the groups).  Latency bounds (3.5 us, of which an empty launch
+// is 2); where few heads have many parts, what a CU fetches, about 35 KB a microsecond: those are cut into slices.
+template <int D, int SLICES>
 __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split sp) {
-  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  constexpr int LANES = D / 4 / SLICES, GROUPS = 256 / LANES, AHEAD = 4;
   __shared__ at_f32x4 part[GROUPS][LANES];
   __shared__ float weights[kTarget + 1], totals[4];
   const int h = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
@@ -332,6 +345,10 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split
     return ((int64_t)(first + i) * sp.heads + head * sp.tiles + g / kRows) * sp.rows + g % kRows;
   };
   const float2* __restrict__ stats = (const float2*)(a.ws + stats_at(sp, D));
+  const int l = threadIdx.x % LANES, group = threadIdx.x / LANES, d = (int)blockIdx.y * (D / SLICES) + 4 * l;
+  at_f32x4 ahead[AHEAD];  // the first sums come while the weights are made
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) ahead[k] = *(const at_f32x4*)(a.ws + slot(min(group + k * GROUPS, parts - 1)) * D + d);
   float most = kNegInf, mine = kNegInf, sum = 0.0f;
   for (int i = threadIdx.x & 63; i < parts; i += 64) most = fmaxf(most, stats[slot(i)].x);
   most = max_xor32(max_xor16(most));
@@ -347,15 +364,16 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split
   for (int x = 1; x < 16; x *= 2) sum += __shfl_xor(sum, x);
   if ((threadIdx.x & 63) == 0) totals[threadIdx.x >> 6] = sum;
   __syncthreads();
-  const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
   at_f32x4 y{0, 0, 0, 0};
-#pragma unroll 4
-  for (int i = group; i < parts; i += GROUPS) {
-    const at_f32x4 v = *(const at_f32x4*)(a.ws + slot(i) * D + 4 * l);
-    const float f = weights[i];
+  auto add = [&](const at_f32x4& v, float f) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] += f * v[j];
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (group + k * GROUPS < parts) add(ahead[k], weights[group + k * GROUPS]);
+#pragma unroll 4
+  for (int i = group + AHEAD * GROUPS; i < parts; i += GROUPS) add(*(const at_f32x4*)(a.ws + slot(i) * D + d), weights[i]);
   part[group][l] = y;
   __syncthreads();
   if (group) return;
@@ -366,7 +384,7 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(AttnArgs a, Split
   }
   const float total = (totals[0] + totals[1]) + (totals[2] + totals[3]);
   const float inv = total == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / total;
-  *(u32x2_t*)(a.out + ((int64_t)b * a.Hq + h) * D + 4 * l) =
+  *(u32x2_t*)(a.out + ((int64_t)b * a.Hq + h) * D + d) =
       u32x2_t{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
 }
 
@@ -377,7 +395,12 @@ void launch(const AttnArgs& a, const Split& sp, hipStream_t stream) {
   auto* kernel = a.kv.f8 ? (split ? attn_decode_kernel<D, true, true> : attn_decode_kernel<D, true, false>)
                          : (split ? attn_decode_kernel<D, false, true> : attn_decode_kernel<D, false, false>);
   kernel<<<units, 64 * kWaves, 0, stream>>>(a, sp);
-  if (split) attn_decode_join_kernel<D><<<(uint32_t)(a.B * a.Hq), 256, 0, stream>>>(a, sp);
+  if (!split) return;
+  const uint32_t rows = (uint32_t)(a.B * a.Hq);
+  // four slices: one token, 40 over 8 heads, 131072 keys 88.4 -> 87.5 us, 32 over one 40.7 -> 37.1; but 1000 keys,
+  // 32 over 8 heads, 8.2 -> 8.5, and 64 ragged sequences 55.3 -> 62.2
+  if (rows < 256 && a.keys > 16384) attn_decode_join_kernel<D, 4><<<dim3(rows, 4), 256, 0, stream>>>(a, sp);
+  else attn_decode_join_kernel<D, 1><<<rows, 256, 0, stream>>>(a, sp);
 }
 
 }  // namespace

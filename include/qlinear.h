@@ -534,7 +534,7 @@ ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void *q, i
  *   int32 [B]; scale > 0; out (dev) bf16 bits [B][Hq][dim]; workspace (dev, 16-byte aligned, contents need not
  *   be zeroed) of qlinear_attn_decode_workspace_bytes, the parts of long sequences; 0 (then NULL will do) if
  *   rows of the table are short.  Calls that share a workspace must not overlap.
- * Hq is a multiple of heads; max_pages * page is below 2^31 (keys, in the size). */
+ * Hq is a multiple of heads; max_pages * page (keys, in the size) is at most 2^30. */
 size_t qlinear_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys);
 ql_status qlinear_attn_decode(const ql_kv_cache *cache, int64_t B, int64_t Hq, const uint16_t *q,
                               const int32_t *table, int64_t table_stride, int64_t max_pages, const int32_t *lens,

@@ -79,7 +79,8 @@ def test_rope_refusals(change, word):
 COMMON = [(dict(B=0), "B"), (dict(B=1 << 24), "B"), (dict(Hq=9), "heads"), (dict(q=None), "null"), (dict(q=ODD), "aligned"),
           (dict(out=ODD), "aligned"), (dict(table=None), "null"), (dict(lens=BAD), "4-byte"), (dict(scale=0.0), "scale"),
           (dict(scale=-1.0), "scale"), (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale"), (dict(most=0), "table"),
-          (dict(stride=8), "table"), (dict(most=1 << 27, stride=1 << 27), "tokens")]
+          (dict(stride=8), "table"), (dict(most=1 << 27, stride=1 << 27), "tokens"),
+          (dict(most=(1 << 26) + 1, stride=(1 << 26) + 1), "tokens")]
 
 
 @pytest.mark.parametrize("change,word", COMMON + [(dict(B=1 << 21, stride=9), "too many"), (dict(most=900, stride=900), "workspace"),

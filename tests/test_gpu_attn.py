@@ -45,6 +45,13 @@ def test_decode_lengths(dev, cache, D, page):
     check_decode(dev, EDGES, 4, 2, D, page, cache, seed=page)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_lengths_in_chunks(dev, cache, D):
+    """The same where one sequence is long enough for all to go by chunks."""
+    check_decode(dev, EDGES + [511, 512, 513, 640, 641], 4, 2, D, 16, cache, seed=D)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (17, 1), (40, 2), (32, 1), (64, 8)])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_decode_heads(dev, Hq, Hkv, cache):
@@ -52,7 +59,8 @@ def test_decode_heads(dev, Hq, Hkv, cache):
     check_decode(dev, [515], Hq, Hkv, 64, 16, cache, seed=Hq + 1)
 
 
-@pytest.mark.parametrize("lens", [[9000], [20011, 3, 0, 513], [1] * 130, [(37 * b) % 1500 for b in range(200)], [65536]])
+@pytest.mark.parametrize("lens", [[9000], [20011, 3, 0, 513], [1] * 130, [(37 * b) % 1500 for b in range(200)], [65536],
+                                  [(13 * b) % 700 for b in range(600)], [257] * 256, [1] * 257 + [3000]])
 @pytest.mark.parametrize("D,cache", [(128, "bf16"), (64, "e4m3")])
 def test_decode_split_and_batches(dev, lens, D, cache):
     check_decode(dev, lens, 4, 1, D, 16, cache, seed=len(lens))
@@ -173,6 +181,19 @@ def test_prompt_rows_that_see_nothing(dev):
 @pytest.mark.parametrize("spread", [8.0, 30.0, 0.0])
 def test_prompt_score_ranges(dev, spread):
     check_prompt(dev, [200, 33], [0, 100], 4, 2, 128, 16, seed=7, spread=spread)
+
+
+def test_prompt_rows_in_front_of_the_first_sequence(dev):
+    """Rows before starts[0], as those behind the last sequence, are left as they were."""
+    seqs = ref.Sequences([40, 9], 1, 64, 16, seed=8)
+    q = ref.queries(60, 2, 64, 9)
+    cache, table, lens = seqs.on(dev)
+    starts = [5, 45, 54]
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device=dev)
+    ql.attn_prompt(q.to(dev), torch.tensor(starts, dtype=torch.int32, device=dev), cache, table, lens, out=out)
+    want, slack = ref.prompt(seqs, q, starts, 64 ** -0.5)
+    close(out[5:54], want[5:54], slack[5:54])
+    assert (out[:5] == 5.0).all() and (out[54:] == 5.0).all()
 
 
 def test_prompt_garbage_behind_the_end(dev):
