@@ -173,6 +173,12 @@ def test_prompt_chunks_and_splits(dev, new, before, D, cache):
     check_prompt(dev, new, before, 4, 2, D, 16, cache, seed=len(new) + D)
 
 
+@pytest.mark.parametrize("B", [64, 65, 140])
+def test_prompt_many_sequences(dev, B):
+    """Of every length, equal ones and empty ones among them: their tiles' order is not the batch's."""
+    check_prompt(dev, [(7 * b) % 40 for b in range(B)], [(37 * b) % 300 if b % 3 else 0 for b in range(B)], 8, 1, 64, 16, seed=B)
+
+
 def test_prompt_rows_that_see_nothing(dev):
     """More queries than tokens: the first see nothing."""
     check_prompt(dev, [20, 200, 3], [-15, -200, -1], 4, 2, 128, 16, seed=4)
