@@ -15,15 +15,18 @@
 //    an order that V's transposing reads (ds_read_b64_tr_b16, four keys of a dim to a lane) follow.
 // A wave has 32 rows, four waves share the keys' tiles in LDS; the next tile is sent for before one is used.
 //
-// 8192 tokens, 32 over 8 heads of 128: 550 us, 1.00 PFLOP/s of what the causal mask leaves, where a large bf16 product
-// reaches 1.50.  Nothing alone bounds: of 3540 cycles that 64 keys of two workgroups take on a CU, the matrix unit is
-// busy 2048 and LDS about 2560 (each wave reads all of K and V: 256 KB, and 64 KB are written), the vector unit
-// half, and the clock follows the power: 1.8 GHz here, 2.4 without load.  Leaving out (in copies) the softmax saves 7 %, the
-// LDS reads 22 %, the loads into LDS 12 %.  Tried and slower or equal: 64 rows a wave, which would halve the reads
-// (512 registers, of which vector instructions reach half: 780 us); 256 rows of eight waves a workgroup (540 against
-// 535); a tile in two halves, one's softmax under the other's products (+ 15 us), also with a fixed order of issue
-// (+ 30); weights made before their maximum is known (+ 15); V's operands read early (- 4, but e4m3 + 13).
+// 8192 tokens, 32 over 8 heads of 128: 520 .. 550 us (by the card), 1.03 PFLOP/s of what the causal mask leaves, where a
+// large bf16 product reaches 1.50.  Nothing alone bounds: of 3500 cycles that 64 keys of two workgroups take on a CU, the
+// matrix unit is busy 2048 and LDS as long (each wave reads all of K and V, V's transposing reads at half the rate of
+// K's: 512 and 1024 cycles, and 64 KB are written), the vector unit half, and the clock follows the power: 1.7 GHz here,
+// 2.4 without load.  More waves at once do not help (three workgroups a CU, with 32 keys a tile: 579 us against 559).
+// Leaving out (in copies) the softmax saves 7 %, the LDS reads 22 %, the loads into LDS 12 %.  Tried and slower or equal:
+// 64 rows a wave, which would halve the reads (512 registers, of which vector instructions reach half: 780 us); 256
+// rows of eight waves a workgroup (540 against 535); a tile in two halves, one's softmax under the other's products
+// (+ 15 us), also with a fixed order of issue (+ 30); weights made before their maximum is known (+ 15); V's operands
+// read early (- 4, but e4m3 + 13); priority for a wave at its products (- 5, but short prompts + 5 %).
 #include <algorithm>
+#include <type_traits>
 
 #include "ql_attn.hpp"
 #include "ql_mx4.hpp"
@@ -37,6 +40,7 @@ constexpr float kLag = 8.0f;     // how far (in powers of two) scores may pass t
 
 struct PromptPlan {
   int G, splits, least;  // least: tiles of keys of a part at least
+  int layer;             // row tiles of 256 workgroups
   int64_t tiles;         // row tiles of a kv head at most
 };
 // Two workgroups fit a CU: where the rows do not make that many, the keys are split.  A part costs its rows' sums
@@ -50,6 +54,7 @@ PromptPlan plan_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t keys) 
   p.least = T * p.G <= 2 * kTileRows ? 4 : 16;
   const int64_t blocks = (T * p.G + kTileRows - 1) / kTileRows * Hkv;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / blocks, keys / (p.least * kTileKeys), kMaxSplits}));
+  p.layer = (int)std::max<int64_t>(1, 256 / (Hkv * p.splits));
   return p;
 }
 
@@ -62,7 +67,9 @@ __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(
 // power of two, seven bits at a time for all lanes.  (16 chunks of 125 tokens behind 375 .. 6000: 175 us, 204 in the
 // batch's order; 13 packed sequences of 47 .. 1183 tokens 89 and 93; 60 of 1 .. 132 21.2 either way.  The longest tiles
 // of all sequences first were slower: workgroups that run together then share no keys.)
-__device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want) {
+// Tiles `layer` .. 2 layer - 1, the second workgroups of the CUs, are taken from their end, so that the longest of the
+// first and the shortest of the second share a CU (2048 tokens, 32 over 8 heads of 128: 52.3 us, then 50.7; 4096: 152, 148).
+__device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want, int layer) {
   const int lane = threadIdx.x & 63;
   uint32_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -88,6 +95,10 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want)
       tiles = __builtin_amdgcn_ds_permute(4 * rank, (int)tiles);
     }
     const uint32_t upto = before + scan_lanes(tiles);
+    if (a.B <= 64 && want >= layer) {
+      const int end = min(2 * layer, (int)last_lane(upto));
+      if (want < end) want = layer + end - 1 - want;
+    }
     const uint64_t here = __ballot((uint32_t)want < upto);
     if (here) {
       const int place = __builtin_ctzll(here), l = __builtin_ctzll(__ballot(rank == place));
@@ -138,6 +149,15 @@ __device__ __forceinline__ void dma_pieces(uint32_t lds, const uint8_t* base, co
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off[0]), "v"(off[1]), "s"(uniform_ptr(base)) : "memory");
 }
 
+// One of them; nothing is read or written where `now` is 0.  Its place among other instructions is kept.
+template <int OFFSET>
+__device__ __forceinline__ void dma_piece(uint32_t now, uint32_t lds, const uint8_t* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_nop 1\n\t"
+               "global_load_lds_dwordx4 %1, %2 offset:%4\n\ts_mov_b64 exec, -1"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform_ptr(base)),
+                  "s"(__builtin_amdgcn_readfirstlane(now)), "n"(OFFSET) : "memory");
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptPlan plan) {
   constexpr int ROW = 2 * D, TILE = kTileKeys * ROW;  // bytes
@@ -148,7 +168,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int Hkv = a.kv.heads, G = plan.G;
   const int split = blockIdx.x % plan.splits, unit = blockIdx.x / plan.splits, head = unit % Hkv;
-  const RowTile rt = find_tile(a, G, unit / Hkv);
+  const RowTile rt = find_tile(a, G, unit / Hkv, plan.layer);
   if (rt.b < 0) return;
   const Keys keys(rt, plan);
   const int t0 = split * keys.per, t1 = min(keys.tiles, t0 + keys.per);
@@ -193,6 +213,10 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   };
   // bf16: straight into LDS, 1 KB (4 or 8 keys) a piece
   constexpr int PIECES = 16 * ROW / 1024, PER = 1024 / ROW;
+  // Eight of them at once keep a wave waiting, so they go out between the first products, two for four (8192 tokens
+  // 557 us, then 551; 1024 26.9 and 26.2).  With heads of 64 half as many products have to hide them: at once (70.6
+  // against 73.7 for 5000 tokens, 10 over 2 heads).
+  constexpr bool SPREAD = !F8 && D == 128;
   uint32_t k_off[PIECES], v_off[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
@@ -278,7 +302,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
     const int bad_now = bad;
     if (t + 1 < t1) {
       next = source(t + 1, ahead);
-      send(next, buf ^ 1);
+      if (!SPREAD || key0 >= limit_last) send(next, buf ^ 1);
       fetch(next);
       ahead = entry(t + 2);
       bad = next.bad;
@@ -324,16 +348,33 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
     if (key0 < limit_last) {
       at_f32x16 s[2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
+      for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[z][e] = 0.0f;
-        const int key = 32 * z + r;
+      const uint32_t now = t + 1 < t1 ? ~0u : 0u, to = lds0 + (buf ^ 1) * 2 * TILE + wave * 16 * ROW;
+      u32x4_t kf[2][4];  // of four products, read four ahead
+      auto k_read = [&](int g) {
+        const int key = 32 * (4 * g / DK) + r;
 #pragma unroll
-        for (int i = 0; i < DK; ++i) {
-          const u32x4_t kf = *(lu32x4p)(kt + key * ROW + (((2 * i + j) ^ swizzle_k<D>(key)) * 16));
-          s[z] = mfma(kf, qf[i], s[z]);
+        for (int i = 0; i < 4; ++i)
+          kf[g & 1][i] = *(lu32x4p)(kt + key * ROW + (((2 * (4 * g % DK + i) + j) ^ swizzle_k<D>(key)) * 16));
+      };
+      auto group = [&](auto of) {
+        constexpr int g = of;
+        if (g + 1 < DK / 2) k_read(g + 1);
+        if constexpr (SPREAD && g < 2) {
+          dma_piece<2048 * g>(now, to, next.k, k_off[2 * g]);
+          dma_piece<2048 * g + 1024>(now, to, next.k, k_off[2 * g + 1]);
+        } else if constexpr (SPREAD) {
+          dma_piece<2048 * (g - 2)>(now, to + TILE, next.v, v_off[2 * (g - 2)]);
+          dma_piece<2048 * (g - 2) + 1024>(now, to + TILE, next.v, v_off[2 * (g - 2) + 1]);
         }
-      }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[4 * g / DK] = mfma(kf[g & 1][i], qf[4 * g % DK + i], s[4 * g / DK]);
+      };
+      k_read(0);
+      group(std::integral_constant<int, 0>{}), group(std::integral_constant<int, 1>{});
+      if constexpr (DK == 8) group(std::integral_constant<int, 2>{}), group(std::integral_constant<int, 3>{});
       const bool masked = key0 + kTileKeys > limit_first || bad_now;
       if (masked) {
         int visible = limit - key0 - 4 * j;
@@ -444,7 +485,7 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, PromptPlan plan) {
   constexpr int LANES = D / 4, ROWS = 256 / LANES;
   const int Hkv = a.kv.heads, G = plan.G, unit = blockIdx.x, head = unit % Hkv;
-  const RowTile rt = find_tile(a, G, unit / Hkv);
+  const RowTile rt = find_tile(a, G, unit / Hkv, plan.layer);
   if (rt.b < 0) return;
   const Keys keys(rt, plan);
   const int parts = keys.parts(), l = threadIdx.x % LANES, row = blockIdx.y * ROWS + threadIdx.x / LANES;
