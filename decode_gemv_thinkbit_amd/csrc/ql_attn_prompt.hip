@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   const int limit = base_pos + query;  // keys that this row sees
   const int limit_first = base_pos + min(rt.row0 + wave * 32, rt.n * G - 1) / G;
   const int limit_tile = base_pos + rt.row0 / G;
-  const int limit_last = base_pos + min(rt.row0 + wave * 32 + 31, rt.n * G - 1) / G;
+  // (a wave without rows sees none: it only brings its keys)
+  const int limit_last = wave * 32 < rows ? base_pos + min(rt.row0 + wave * 32 + 31, rt.n * G - 1) / G : 0;
 
   u32x4_t qf[DK];
   {
