@@ -64,8 +64,8 @@ struct RowTile {
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
 // Number `want` of all sequences' tiles: of 64 sequences those with the most keys first, and a sequence's last tile,
 // which sees the most keys, first, so that short tiles fill the end.  Lengths are compared in steps of a quarter of a
-// power of two, seven bits at a time for all lanes.  (16 chunks of 125 tokens behind 375 .. 6000: 175 us, 204 in the
-// batch's order; 13 packed sequences of 47 .. 1183 tokens 89 and 93; 60 of 1 .. 132 21.2 either way.  The longest tiles
+// power of two, seven bits at a time for all lanes.  (16 chunks of 7 .. 250 tokens behind 375 .. 6000: 175 us, 204 in the
+// batch's order; 13 packed sequences of 47 .. 1189 tokens 89 and 93; 60 of 1 .. 158 21.2 either way.  The longest tiles
 // of all sequences first were slower: workgroups that run together then share no keys.)
 // Tiles `layer` .. 2 layer - 1, the second workgroups of the CUs, are taken from their end, so that the longest of the
 // first and the shortest of the second share a CU (2048 tokens, 32 over 8 heads of 128: 52.3 us, then 50.7; 4096: 152, 148).
@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
     }
   if (whole) {
     // Through LDS, so that rows lie in memory as they are written, 16 bytes a lane (8 bytes of 32 rows at a time,
-    // straight from the registers, took 2 us a row tile: 13 packed sequences of 47 .. 1184 tokens 97 us against 93,
-    // 60 of 1 .. 132 22.3 against 20.3).  Each wave has its rows' part of the buffer that all waves had left before
+    // straight from the registers, took 2 us a row tile: 13 packed sequences of 47 .. 1189 tokens 97 us against 93,
+    // 60 of 1 .. 158 22.3 against 20.3).  Each wave has its rows' part of the buffer that all waves had left before
     // the last tile.
     constexpr int COLS = ROW / 16, AT = 64 / COLS;
     uint8_t* stage = smem + ((t1 - t0) & 1) * 2 * TILE + wave * 32 * ROW;
