@@ -52,6 +52,10 @@ typedef __attribute__((ext_vector_type(4))) float at_f32x4;
 typedef __attribute__((ext_vector_type(16))) float at_f32x16;
 
 constexpr float kNegInf = -__builtin_inff();
+// Weights are exp2(score - maximum - kRoom): up to 2^8 by the maximum in use, so that 2^30 of them times the largest values
+// stay in fp32's range (2^30 2^128 2^8 2^-39 = 2^127).  The factor cancels out; a weight's exponent is rounded in
+// steps of 2^-18, 2^-19 off, where a bf16 weight is off by 2^-9.
+constexpr float kRoom = 39.0f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -66,7 +66,8 @@ __device__ __forceinline__ Place find_place(const int32_t* __restrict__ lens, in
     read(b0);
     total += last_lane(scan_lanes(steps(len[0]) + steps(len[1]) + steps(len[2]) + steps(len[3])));
   }
-  const uint32_t c = (uint32_t)(((uint64_t)total * (uint32_t)heads + kTarget - 1) / kTarget);
+  // (2^23 steps hold the longest sequence)
+  const uint32_t c = (uint32_t)min(((uint64_t)total * (uint32_t)heads + kTarget - 1) / kTarget, (uint64_t)1 << 23);
   uint32_t before = 0;
   for (int b0 = 0; b0 < B; b0 += 256) {
     if (b0) read(b0);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
     const float m_new = fmaxf(m, top);
     const float alpha = part_weight(m, m_new);
     m = m_new;
-    const float base = m == kNegInf ? 0.0f : m;
+    const float base = m == kNegInf ? 0.0f : m + kRoom;
     sum *= alpha;
 #pragma unroll
     for (int i = 0; i < NB; ++i)

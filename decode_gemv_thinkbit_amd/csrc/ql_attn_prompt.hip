@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
       for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
       top = max_xor32(top) * c;
       // The maximum in use follows only when some row's scores pass it by 2^kLag (the result is the same: it
-      // cancels out, and sums of exp2 below 2^8 each keep far from fp32's end)
+      // cancels out, and kRoom has place for weights of 2^8)
       if (__ballot(top > m + kLag)) {
         const float m_new = fmaxf(m, top), alpha = part_weight(m, m_new);
         m = m_new;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
       }
-      const float base = m == kNegInf ? 0.0f : m;
+      const float base = m == kNegInf ? 0.0f : m + kRoom;
       u32x4_t pf[4];
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {

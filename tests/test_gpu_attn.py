@@ -121,6 +121,33 @@ def test_decode_infinite_values(dev):
     assert torch.equal(got[0][:, keep], want[0][:, keep])
 
 
+def of_large_values(seqs):
+    """V as large as its type allows: sums of a few would pass fp32's end."""
+    most = 2.0 ** 125
+    seqs.v = seqs.v.abs() * most
+    for both in seqs.kv:
+        both[1] = both[1].abs() * most
+    return seqs
+
+
+@pytest.mark.parametrize("lens", [[500], [700, 3, 40], [9000]])
+def test_decode_large_values(dev, lens):
+    seqs = of_large_values(ref.Sequences(lens, 2, 64, 16, seed=5))
+    q = ref.queries(len(lens), 4, 64, 6)
+    want, slack = ref.decode(seqs, q, 64 ** -0.5)
+    close(ql.attn_decode(q.to(dev), *seqs.on(dev)), want, slack)
+
+
+@pytest.mark.parametrize("n,length", [(300, 300), (5, 4000)])
+def test_prompt_large_values(dev, n, length):
+    seqs = of_large_values(ref.Sequences([length], 2, 128, 16, seed=5))
+    q = ref.queries(n, 4, 128, 6)
+    cache, table, lens = seqs.on(dev)
+    got = ql.attn_prompt(q.to(dev), torch.tensor([0, n], dtype=torch.int32, device=dev), cache, table, lens)
+    want, slack = ref.prompt(seqs, q, [0, n], 128 ** -0.5)
+    close(got, want, slack)
+
+
 def test_decode_equal_scores_average(dev):
     """Equal keys: the mean of V."""
     n = 777
