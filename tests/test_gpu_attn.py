@@ -206,6 +206,13 @@ def test_prompt_many_sequences(dev, B):
     check_prompt(dev, [(7 * b) % 40 for b in range(B)], [(37 * b) % 300 if b % 3 else 0 for b in range(B)], 8, 1, 64, 16, seed=B)
 
 
+@pytest.mark.parametrize("new,before,Hq,Hkv", [([2500], [0], 16, 16), ([4200], [0], 16, 16), ([1500, 9, 1100], [0, 0, 0], 16, 8),
+                                               ([500], [5000], 16, 4), ([400, 130], [4000, 6000], 8, 4)])
+def test_prompt_more_tiles_than_first_workgroups(dev, new, before, Hq, Hkv):
+    """More row tiles than the CUs take at first: the others' order differs, in parts of rows too."""
+    check_prompt(dev, new, before, Hq, Hkv, 64, 64, seed=len(new))
+
+
 def test_prompt_rows_that_see_nothing(dev):
     """More queries than tokens: the first see nothing."""
     check_prompt(dev, [20, 200, 3], [-15, -200, -1], 4, 2, 128, 16, seed=4)
