@@ -13,7 +13,8 @@
 //  - output of dims x rows: V, transposed, is the first operand, and the scores are the second one as they
 //    are: registers 8 h .. 8 h + 7 of a 32-key tile are the 16 keys 16 h + 8 (e / 4) + 4 j + e % 4, e < 8, in
 //    an order that V's transposing reads (ds_read_b64_tr_b16, four keys of a dim to a lane) follow.
-// A wave has 32 rows, four waves share the keys' tiles in LDS; the next tile is sent for before one is used.
+// A wave has 32 rows, four waves share the keys' tiles in LDS; the next tile is sent for before one is used.  Two such
+// groups may take turns at a row tile's keys; their sums are joined in LDS, as parts of split rows are through memory.
 //
 // 8192 tokens, 32 over 8 heads of 128: 520 .. 550 us (by the card), 1.03 PFLOP/s of what the causal mask leaves, where a
 // large bf16 product reaches 1.50.  Nothing alone bounds: of 3500 cycles that 64 keys of two workgroups take on a CU, the
@@ -41,6 +42,7 @@ constexpr float kLag = 8.0f;     // how far (in powers of two) scores may pass t
 struct PromptPlan {
   int G, splits, least;  // least: tiles of keys of a part at least
   int layer;             // row tiles of 256 workgroups
+  int groups;            // of four waves
   int64_t tiles;         // row tiles of a kv head at most
 };
 // Two workgroups fit a CU: where the rows do not make that many, the keys are split.  A part costs its rows' sums
@@ -54,7 +56,17 @@ PromptPlan plan_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t keys) 
   p.least = T * p.G <= 2 * kTileRows ? 4 : 16;
   const int64_t blocks = (T * p.G + kTileRows - 1) / kTileRows * Hkv;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / blocks, keys / (p.least * kTileKeys), kMaxSplits}));
-  p.layer = (int)std::max<int64_t>(1, 256 / (Hkv * p.splits));
+  // Where a CU gets one workgroup or little more, two groups of waves take turns at a row tile's keys: 1024 tokens, 32 over
+  // 8 heads of 128, 26.4 us, then 23.5; 512 15.8 and 15.2; 200 behind 3000 33.9 and 30.2; with two workgroups for a CU,
+  // 1500 tokens 37.0 and 33.4, 2048 49.5 and 47.1, with more no longer (3000 84.0 and 94.8).  Joining them takes 2 us, too
+  // much for short rows (200 tokens 10.1 and 11.1; four sequences of 125 .. 875 26.3 and 30.5) and for the short parts of
+  // few rows (16 behind 16000 29.0 and 30.0).
+  const int64_t units = (T * p.G + (B - 1) * (kTileRows / 2) + kTileRows - 1) / kTileRows * Hkv * p.splits;  // about
+  const bool two = p.splits > 1    ? units <= 256 && T * p.G > 2 * kTileRows
+                   : units <= 256 ? T >= 300 * B
+                                  : units <= 512 && T >= 1000 * B;
+  p.groups = two ? 2 : 1;
+  p.layer = two ? 1 << 24 : (int)std::max<int64_t>(1, 256 / (Hkv * p.splits));
   return p;
 }
 
@@ -67,8 +79,9 @@ __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(
 // power of two, seven bits at a time for all lanes.  (16 chunks of 7 .. 250 tokens behind 375 .. 6000: 175 us, 204 in the
 // batch's order; 13 packed sequences of 47 .. 1189 tokens 89 and 93; 60 of 1 .. 158 21.2 either way.  The longest tiles
 // of all sequences first were slower: workgroups that run together then share no keys.)
-// Tiles `layer` .. 2 layer - 1, the second workgroups of the CUs, are taken from their end, so that the longest of the
-// first and the shortest of the second share a CU (2048 tokens, 32 over 8 heads of 128: 52.3 us, then 50.7; 4096: 152, 148).
+// Tiles `layer` .. 2 layer - 1, the second workgroups of the CUs (of one group of waves), are taken from their end, so
+// that the longest of the first and the shortest of the second share a CU (4096 tokens, 32 over 8 heads of 128: 148 us,
+// 152 without).
 __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want, int layer) {
   const int lane = threadIdx.x & 63;
   uint32_t before = 0;
@@ -158,14 +171,17 @@ __device__ __forceinline__ void dma_piece(uint32_t now, uint32_t lds, const uint
                   "s"(__builtin_amdgcn_readfirstlane(now)), "n"(OFFSET) : "memory");
 }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptPlan plan) {
+template <int D, bool F8, int GROUPS>
+__global__ void __launch_bounds__(256 * GROUPS, 2) attn_prompt_kernel(AttnArgs a, PromptPlan plan) {
   constexpr int ROW = 2 * D, TILE = kTileKeys * ROW;  // bytes
   constexpr int DK = D / 16, DT = D / 32;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * TILE];  // K, V, K, V
-  __shared__ uint32_t odd_bits[2][kTileKeys][DT], odd_waves[4];
+  __shared__ __attribute__((aligned(1024))) uint8_t all[GROUPS * 4 * TILE];  // of each group: K, V, K, V
+  __shared__ uint32_t all_odd_bits[GROUPS][2][kTileKeys][DT], odd_waves[GROUPS][4];
   const int lane = threadIdx.x & 63, j = lane >> 5, r = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+  uint8_t* smem = all + group * 4 * TILE;
+  auto& odd_bits = all_odd_bits[group];
   const int Hkv = a.kv.heads, G = plan.G;
   const int split = blockIdx.x % plan.splits, unit = blockIdx.x / plan.splits, head = unit % Hkv;
   const RowTile rt = find_tile(a, G, unit / Hkv, plan.layer);
@@ -183,9 +199,9 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   // group w.  A group behind the last key takes the last key's page; entries that are no page read page 0 and
   // are masked (bit g of `bad`).
   const int key_last = max(1, min(rt.len, kTileKeys * keys.tiles)) - 1;
-  auto entry = [&](int t) { return row[min(t * kTileKeys + 16 * (lane & 3), key_last) >> shift]; };
+  auto entry = [&](int t) { return row[min(t * kTileKeys + 16 * (lane & (4 * GROUPS - 1)), key_last) >> shift]; };
   int now = 0, ahead = 0;
-  if (t0 < t1) now = entry(t0), ahead = entry(t0 + 1);
+  if (t0 < t1) now = entry(t0), ahead = entry(t0 + GROUPS);
 
   const int rows = rt.n * G - rt.row0;  // those of the tile, or more
   const int base_pos = rt.len - rt.n + 1;
@@ -207,10 +223,10 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
 
   struct Source { const uint8_t *k, *v; int bad; };
   auto source = [&](int t, int e) {
-    const int own = __builtin_amdgcn_readlane(e, wave);
+    const int own = __builtin_amdgcn_readlane(e, 4 * group + wave);
     const int page = (uint32_t)own < (uint32_t)a.kv.pages ? own : 0;
     const int64_t off = ((((int64_t)page * Hkv + head) << shift) + ((t * kTileKeys + 16 * wave) & in_page)) * (int64_t)(F8 ? D : 2 * D);
-    return Source{a.kv.k + off, a.kv.v + off, (int)(__ballot((uint32_t)e >= (uint32_t)a.kv.pages) & 15)};
+    return Source{a.kv.k + off, a.kv.v + off, (int)(__ballot((uint32_t)e >= (uint32_t)a.kv.pages) & (GROUPS == 1 ? 15 : 255))};
   };
   // bf16: straight into LDS, 1 KB (4 or 8 keys) a piece
   constexpr int PIECES = 16 * ROW / 1024, PER = 1024 / ROW;
@@ -285,7 +301,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   Source next = {};
   int bad = 0;
   if (t0 < t1) {
-    next = source(t0, now);
+    next = source(t0 + group, now);
     send(next, 0);
     fetch(next);
     put(0);
@@ -294,26 +310,27 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
   // q has come here, not in the loop: there a wait for it would be one for the loads into LDS too
 #pragma unroll
   for (int i = 0; i < DK; ++i) asm volatile("" : "+v"(qf[i]));
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1, key0 = t * kTileKeys;
+  for (int first = t0; first < t1; first += GROUPS) {
+    const int t = first + group, buf = (first - t0) / GROUPS & 1, key0 = t * kTileKeys;
+    const bool more = first + GROUPS < t1;
     const uint8_t *kt = smem + buf * 2 * TILE, *vt = kt + TILE;
     wait_vm<0>();
     wait_lgkm();
     barrier();
-    const int bad_now = bad;
-    if (t + 1 < t1) {
-      next = source(t + 1, ahead);
+    const int bad_any = bad, bad_now = bad >> (4 * group) & 15;
+    if (more) {
+      next = source(t + GROUPS, ahead);
       if (!SPREAD || key0 >= limit_last) send(next, buf ^ 1);
       fetch(next);
-      ahead = entry(t + 2);
+      ahead = entry(first + 2 * GROUPS);
       bad = next.bad;
     }
     // 0 * inf is NaN, also where a weight is 0 because the row does not see the key, and what memory behind the
     // last key holds is anything.  So in tiles that not every row sees whole, values that are not finite are taken
     // out of V, and noted: bit d % 32 of word d / 32 of a key, for +inf, -inf and (both) NaN.
     bool odd = false;
-    if (key0 + kTileKeys > limit_tile || bad_now) {
-      const int key = threadIdx.x / DT, dt = threadIdx.x % DT;
+    if ((first + GROUPS) * kTileKeys > limit_tile || bad_any) {
+      const int key = threadIdx.x % 256 / DT, dt = threadIdx.x % DT;
       bool found = false;
       if (key < kTileKeys) {
         uint32_t up = 0, down = 0;
@@ -342,17 +359,17 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
         odd_bits[0][key][dt] = up, odd_bits[1][key][dt] = down;
       }
       const bool any = __ballot(found) != 0;
-      if (lane == 0) odd_waves[wave] = any;
+      if (lane == 0) odd_waves[group][wave] = any;
       __syncthreads();
-      odd = odd_waves[0] | odd_waves[1] | odd_waves[2] | odd_waves[3];
+      odd = odd_waves[group][0] | odd_waves[group][1] | odd_waves[group][2] | odd_waves[group][3];
     }
-    if (key0 < limit_last) {
+    if (key0 < limit_last && (GROUPS == 1 || t < t1)) {
       at_f32x16 s[2];
 #pragma unroll
       for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[z][e] = 0.0f;
-      const uint32_t now = t + 1 < t1 ? ~0u : 0u, to = lds0 + (buf ^ 1) * 2 * TILE + wave * 16 * ROW;
+      const uint32_t now = more ? ~0u : 0u, to = lds0 + (buf ^ 1) * 2 * TILE + wave * 16 * ROW;
       u32x4_t kf[2][4];  // of four products, read four ahead
       auto k_read = [&](int g) {
         const int key = 32 * (4 * g / DK) + r;
@@ -432,11 +449,40 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
         }
       }
     }
-    if (t + 1 < t1) put(buf ^ 1);
+    if (more) put(buf ^ 1);
   }
   wait_vm<0>();
 
   sum = sum_xor32(sum);
+  if constexpr (GROUPS == 2) {  // the second group's sums to the first, through LDS
+    const int at = threadIdx.x % 256;
+    at_f32x4* sums = (at_f32x4*)(all + 4 * TILE) + wave * (4 * DT * 64) + lane;
+    float* rest = (float*)(all + 2 * TILE) + at;
+    __syncthreads();
+    if (group) {
+#pragma unroll
+      for (int i = 0; i < 4 * DT; ++i) {
+        const at_f32x16& x = o[i / 4];
+        sums[i * 64] = at_f32x4{x[i % 4 * 4], x[i % 4 * 4 + 1], x[i % 4 * 4 + 2], x[i % 4 * 4 + 3]};
+      }
+      rest[0] = m, rest[256] = sum;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) rest[512 + 256 * dt] = __uint_as_float(infinities[dt]);
+    }
+    __syncthreads();
+    if (group) return;
+    const float m1 = rest[0], most = fmaxf(m, m1), f0 = part_weight(m, most), f1 = part_weight(m1, most);
+    sum = f0 * sum + f1 * rest[256];
+    m = most;
+#pragma unroll
+    for (int i = 0; i < 4 * DT; ++i) {
+      const at_f32x4 x = sums[i * 64];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i / 4][i % 4 * 4 + e] = f0 * o[i / 4][i % 4 * 4 + e] + f1 * x[e];
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) infinities[dt] |= __float_as_uint(rest[512 + 256 * dt]);
+  }
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
     if (infinities[dt]) {
@@ -452,7 +498,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(AttnArgs a, PromptP
     // 60 of 1 .. 158 22.3 against 20.3).  Each wave has its rows' part of the buffer that all waves had left before
     // the last tile.
     constexpr int COLS = ROW / 16, AT = 64 / COLS;
-    uint8_t* stage = smem + ((t1 - t0) & 1) * 2 * TILE + wave * 32 * ROW;
+    uint8_t* stage = smem + (GROUPS == 1 ? (t1 - t0) & 1 : 0) * 2 * TILE + wave * 32 * ROW;
     auto place = [&](int row, int col) { return stage + row * ROW + (col ^ (row % COLS)) * 16; };
     const float inv = sum == 0.0f ? 0.0f : (a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / sum;
 #pragma unroll
@@ -531,8 +577,12 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, Promp
 template <int D>
 void launch(const AttnArgs& a, const PromptPlan& p, hipStream_t stream) {
   const uint32_t blocks = (uint32_t)(p.tiles * a.kv.heads);
-  if (a.kv.f8) attn_prompt_kernel<D, true><<<blocks * p.splits, 256, 0, stream>>>(a, p);
-  else attn_prompt_kernel<D, false><<<blocks * p.splits, 256, 0, stream>>>(a, p);
+  auto run = [&](auto f8) {
+    if (p.groups == 2) attn_prompt_kernel<D, f8, 2><<<blocks * p.splits, 512, 0, stream>>>(a, p);
+    else attn_prompt_kernel<D, f8, 1><<<blocks * p.splits, 256, 0, stream>>>(a, p);
+  };
+  if (a.kv.f8) run(std::true_type{});
+  else run(std::false_type{});
   if (p.splits > 1) attn_prompt_join_kernel<D><<<dim3(blocks, kTileRows * D / 1024), 256, 0, stream>>>(a, p);
 }
 

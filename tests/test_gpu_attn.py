@@ -138,7 +138,7 @@ def test_decode_large_values(dev, lens):
     close(ql.attn_decode(q.to(dev), *seqs.on(dev)), want, slack)
 
 
-@pytest.mark.parametrize("n,length", [(300, 300), (5, 4000)])
+@pytest.mark.parametrize("n,length", [(200, 200), (300, 300), (700, 700), (5, 4000), (300, 4000)])
 def test_prompt_large_values(dev, n, length):
     seqs = of_large_values(ref.Sequences([length], 2, 128, 16, seed=5))
     q = ref.queries(n, 4, 128, 6)
@@ -207,7 +207,8 @@ def test_prompt_many_sequences(dev, B):
 
 
 @pytest.mark.parametrize("new,before,Hq,Hkv", [([2500], [0], 16, 16), ([4200], [0], 16, 16), ([1500, 9, 1100], [0, 0, 0], 16, 8),
-                                               ([500], [5000], 16, 4), ([400, 130], [4000, 6000], 8, 4)])
+                                               ([500], [5000], 16, 4), ([400, 130], [4000, 6000], 8, 4), ([1300], [0], 16, 16),
+                                               ([1700], [0], 24, 8)])
 def test_prompt_more_tiles_than_first_workgroups(dev, new, before, Hq, Hkv):
     """More row tiles than the CUs take at first: the others' order differs, in parts of rows too."""
     check_prompt(dev, new, before, Hq, Hkv, 64, 64, seed=len(new))
@@ -288,6 +289,41 @@ def test_prompt_bad_pages(dev):
     got = ql.attn_prompt(q.to(dev), torch.tensor(starts, dtype=torch.int32, device=dev), cache, table, lens)
     want, slack = ref.prompt(seqs, q, starts, 128 ** -0.5, visible)
     close(got, want, slack)
+
+
+@pytest.mark.parametrize("D,G,cache", [(128, 2, "bf16"), (64, 3, "bf16"), (128, 1, "e4m3")])
+def test_prompt_long_rows_infinities_and_bad_pages(dev, D, G, cache):
+    """Rows long enough for two groups of waves, of which each has every second tile of 64 keys."""
+    n = 450
+    seqs = ref.Sequences([n], 1, D, 16, cache, seed=3)
+    q = ref.queries(n, G, D, 4)
+    kv, table, lens = seqs.on(dev)
+    starts = torch.tensor([0, n], dtype=torch.int32, device=dev)
+    call = lambda: ql.attn_prompt(q.to(dev), starts, kv, table, lens)
+    visible = torch.ones(n, dtype=torch.bool)
+    for i, e in {1: -1, 5: 10 ** 9, 14: -7, 23: seqs.k.shape[0]}.items():
+        table[0, i] = e
+        visible[16 * i : 16 * i + 16] = False
+    want = call()
+    exact, slack = ref.prompt(seqs, q, [0, n], D ** -0.5, {0: visible})
+    close(want, exact, slack)
+
+    def put(t, at, d, x):
+        t.view(torch.uint8 if cache == "e4m3" else t.dtype)[seqs.table[0, at // 16].item(), 0, at % 16, d] = x
+
+    nan = 0x7F if cache == "e4m3" else NAN
+    expect = want.clone()
+    for at, d in ((50, 7), (100, 9), (330, 3), (449, 60)):
+        put(kv.v, at, d, nan)
+        expect[at:, :, d] = NAN
+    if cache == "bf16":
+        for at, d, x in ((70, 33, INF), (140, 33, -INF), (200, 40, -INF), (270, 40, -INF)):
+            put(kv.v, at, d, x)
+            expect[at:, :, d] = NAN if at == 140 else x
+    put(kv.v, 20, 11, nan)  # of a page that is not seen
+    got = call()
+    assert torch.equal(torch.isnan(got), torch.isnan(expect))
+    assert torch.equal(torch.nan_to_num(got, nan=3.0), torch.nan_to_num(expect, nan=3.0))
 
 
 def test_prompt_starts_are_cut(dev):
