@@ -151,10 +151,10 @@ template <int D> __device__ __forceinline__ int swizzle_v(int key) { return D ==
 // off[i]: the lane's place in piece i.  As for the loads in ql_mx4.hpp, readers wait, and the wait states are kept here.
 __device__ __forceinline__ void dma_pieces(uint32_t lds, const uint8_t* base, const uint32_t (&off)[4]) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
-               "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-               "global_load_lds_dwordx4 %4, %5 offset:3072"
+               "global_load_lds_dwordx4 %2, %5 offset:%6\n\tglobal_load_lds_dwordx4 %3, %5 offset:2*%6\n\t"
+               "global_load_lds_dwordx4 %4, %5 offset:3*%6"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]),
-                  "s"(uniform_ptr(base)) : "memory");
+                  "s"(uniform_ptr(base)), "n"(1024) : "memory");
 }
 __device__ __forceinline__ void dma_pieces(uint32_t lds, const uint8_t* base, const uint32_t (&off)[2]) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
