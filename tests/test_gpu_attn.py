@@ -516,3 +516,70 @@ def test_prompt_then_decode(dev):
     for b, n in enumerate(new):
         seqs.kv[b] = [t[: n + 1] for t in full[b]]
     close(out1, *ref.decode(seqs, q1.cpu().view(3, Hq, D), D ** -0.5))
+
+
+@pytest.mark.parametrize("B,capacity", [(1, 1280), (3, 1280), (1, 4096), (2, 4096)])
+def test_prompt_chunks_replayed(dev, B, capacity):
+    """Chunks of packed prompts through rope_append and attn_prompt in one captured graph: other lengths, positions and
+    values each time, eager work between, the bits of eager calls on a cache of their own."""
+    T, Hq, Hkv, D, page = 320, 4, 2, 64, 16
+    g = torch.Generator().manual_seed(71)
+    pages = B * capacity // page
+    table = torch.randperm(pages, generator=g).int().view(B, -1)
+    caches = [ql.KvCache(*(torch.zeros(pages, Hkv, page, D, dtype=torch.bfloat16, device=dev) for _ in "kv")) for _ in "ab"]
+    rope = ql.Rope(ql.rope_frequencies(D)[0].to(dev))
+    q, k, v = (torch.zeros(T, h, D, device=dev) for h in (Hq, Hkv, Hkv))
+    positions, slots = (torch.full((T,), -1, dtype=torch.int32, device=dev) for _ in "ps")
+    starts, lens = torch.zeros(B + 1, dtype=torch.int32, device=dev), torch.zeros(B, dtype=torch.int32, device=dev)
+    at, out = table.to(dev), torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
+
+    def step(cache):
+        return ql.attn_prompt(ql.rope_append(q, k, v, positions, slots, rope, cache), starts, cache, at, lens, out=out)
+
+    done = [0] * B
+
+    def fill(i):
+        cuts = sorted(torch.randint(0, T - 9, (B - 1,), generator=g).tolist())
+        new = [b - a for a, b in zip([0] + cuts, cuts + [T - 5 * i])]  # the last rows are nobody's
+        p, s, begin = [], [], [0]
+        for b in range(B):
+            where = torch.arange(done[b], done[b] + new[b])
+            p.append(where)
+            s.append(table[b, where // page] * page + where % page)
+            done[b] += new[b]
+            begin.append(begin[-1] + new[b])
+        rest = T - begin[-1]
+        positions.copy_(torch.cat(p + [torch.zeros(rest)]).int())
+        slots.copy_(torch.cat(s + [torch.full((rest,), -1)]).int())
+        starts.copy_(torch.tensor(begin).int())
+        lens.copy_(torch.tensor(done).int())
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g))
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):  # no token has a slot, no sequence a row
+        step(caches[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(caches[1])
+    for c in caches:
+        c.k.zero_(), c.v.zero_()
+    for i in range(3):
+        fill(i)
+        out.fill_(5.0)
+        want = step(caches[0]).clone()
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+        torch.randn(1000, device=dev).sum()
+    n = starts.tolist()
+    turned = ql.rope_append(q, k, v, positions, slots, rope, caches[0]).cpu()
+    seqs = ref.Sequences([0] * B, Hkv, D, page)
+    for b in range(B):
+        seqs.kv[b] = [t.float().cpu()[table[b].long()].transpose(1, 2).reshape(-1, Hkv, D)[: done[b]].double()
+                      for t in (caches[0].k, caches[0].v)]
+    want, slack = ref.prompt(seqs, turned, n, D ** -0.5)
+    close(out[: n[-1]], want[: n[-1]], slack[: n[-1]])
+    assert (out[n[-1] :] == 5.0).all()
