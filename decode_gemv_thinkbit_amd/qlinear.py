@@ -972,9 +972,10 @@ def attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lens: torc
         raise ValueError(f"q has {rows} rows, the table {B}")
     out = _result(out, q.shape, torch.bfloat16, device)
     need = _workspace_bytes("attn_decode", device, B, Hq, Hkv, D, most * page)
-    workspace = _scratch(workspace, need, device).data_ptr() if need else None
+    workspace = _scratch(workspace, need, device) if need else None
     _launch("attn_decode", lib().qlinear_attn_decode, device, cache.desc, B, Hq, q.data_ptr(), table.data_ptr(),
-            table.stride(0), most, _int32(lens, B, device, "lens"), scale, out.data_ptr(), workspace, need)
+            table.stride(0), most, _int32(lens, B, device, "lens"), scale, out.data_ptr(),
+            workspace.data_ptr() if need else None, need)
     return out
 
 
@@ -988,10 +989,10 @@ def attn_prompt(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, table: to
     device, Hkv, page, D, T, Hq, B, most, scale = _attention(q, cache, table, lens, scale)
     out = _result(out, q.shape, torch.bfloat16, device)
     need = _workspace_bytes("attn_prompt", device, T, B, Hq, Hkv, D, most * page)
-    workspace = _scratch(workspace, need, device).data_ptr() if need else None
+    workspace = _scratch(workspace, need, device) if need else None
     _launch("attn_prompt", lib().qlinear_attn_prompt, device, cache.desc, T, B, Hq, q.data_ptr(),
             _int32(starts, B + 1, device, "starts"), table.data_ptr(), table.stride(0), most,
-            _int32(lens, B, device, "lens"), scale, out.data_ptr(), workspace, need)
+            _int32(lens, B, device, "lens"), scale, out.data_ptr(), workspace.data_ptr() if need else None, need)
     return out
 
 
