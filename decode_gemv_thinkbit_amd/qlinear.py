@@ -798,7 +798,8 @@ _pack_rope = struct.Struct("@P2ifi").pack  # ql_rope
 @dataclass(frozen=True, eq=False, init=False)
 class KvCache:
     """A paged key-value cache: k, v [pages, heads, page, D], bf16, or float8_e4m3fn with one scale per head (a
-    stored x stands for x * scale).  Slot number i is place i % page of page i // page."""
+    stored x stands for x * scale).  Slot number i is place i % page of page i // page.  Tensors that are given other
+    memory (set_, .data, a resized storage) are checked and used there from the next call on."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: Optional[torch.Tensor]  # fp32 [heads], positive; e4m3 only
@@ -833,8 +834,17 @@ class KvCache:
                         s.device != device:
                     raise ValueError(f"k_scale and v_scale must be float32 [{heads}], contiguous, on the cache's device")
             scales = k_scale.data_ptr(), v_scale.data_ptr()
+        at = k.data_ptr(), v.data_ptr(), *scales
         self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, shape=(pages, heads, page, D), device=device,
-                             desc=_pack_cache(pages, heads, page, D, kind, 0, k.data_ptr(), v.data_ptr(), *scales))
+                             at=at, desc=_pack_cache(pages, heads, page, D, kind, 0, *at))
+
+    def current(self) -> "KvCache":
+        """The cache, `desc` made anew if the tensors have other memory than when it was made."""
+        at = self.at
+        if self.k.data_ptr() != at[0] or self.v.data_ptr() != at[1] or \
+                (at[2] and (self.k_scale.data_ptr() != at[2] or self.v_scale.data_ptr() != at[3])):
+            self.__init__(self.k, self.v, self.k_scale, self.v_scale)
+        return self
 
     @property
     def nbytes(self) -> int:
@@ -854,8 +864,15 @@ class Rope:
         shape = freqs.shape
         if freqs.dtype is not torch.float32 or len(shape) != 1 or not shape[0] or not freqs.is_contiguous():
             raise ValueError("freqs must be float32 [pairs], contiguous")
-        self.__dict__.update(freqs=freqs, interleaved=interleaved, factor=factor, device=freqs.device,
-                             desc=_pack_rope(freqs.data_ptr(), 2 * shape[0], 1 if interleaved else 0, factor, 0))
+        at = freqs.data_ptr()
+        self.__dict__.update(freqs=freqs, interleaved=interleaved, factor=factor, device=freqs.device, at=at,
+                             desc=_pack_rope(at, 2 * shape[0], 1 if interleaved else 0, factor, 0))
+
+    def current(self) -> "Rope":
+        """As KvCache's."""
+        if self.freqs.data_ptr() != self.at:
+            self.__init__(self.freqs, self.interleaved, self.factor)
+        return self
 
 
 def rope_frequencies(dims: int, base: float = 10000.0, stretch: float = 1.0, original: Optional[int] = None,
@@ -893,7 +910,7 @@ def _cache(cache: KvCache, device: torch.device):
     """The device's cache's (pages, heads, page, D)."""
     if not isinstance(cache, KvCache):
         raise ValueError("cache must be a KvCache")
-    if cache.device != device or device.type != "cuda":
+    if cache.current().device != device or device.type != "cuda":
         raise ValueError("the operands and the cache must be on one CUDA (HIP) device")
     return cache.shape
 
@@ -937,7 +954,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     of_k, of_v = _rows(k, D, "k"), _rows(v, D, "v")
     if of_k[:2] != (T, Hkv) or of_v[:2] != (T, Hkv) or k.device != device or v.device != device:
         raise ValueError(f"k and v must be [{T}, {Hkv}, {D}] on {device}")
-    if not isinstance(rope, Rope) or rope.device != device:
+    if not isinstance(rope, Rope) or rope.current().device != device:
         raise ValueError(f"rope must be a Rope with its frequencies on {device}")
     out = _result(out, q.shape, torch.bfloat16, device)
     _launch("rope_append", lib().qlinear_rope_append, device, T, Hq, kind, q.data_ptr(), q_stride, k.data_ptr(), of_k[2],
