@@ -139,6 +139,17 @@ struct Keys {
   __device__ __forceinline__ int parts() const { return max(1, (tiles + per - 1) / per); }
 };
 
+// The workspace, where rows are split: [part][kv head][row][D] sums of exp2(s - m) v, then [part][kv head][row][2] m and
+// sum; a row is one of the T * G (query, head) pairs.  Rows that are split fill 512 tiles at most, so this is 34 MB at
+// most, however few rows a tile has.
+struct Parts {
+  int64_t rows;  // T * G
+  int heads, splits;
+  __host__ __device__ int64_t at(int head, int split, int64_t row) const { return ((int64_t)split * heads + head) * rows + row; }
+  __host__ __device__ int64_t stats(int D) const { return splits * heads * rows * D; }
+  __host__ __device__ int64_t size(int D) const { return splits * heads * rows * (D + 2); }
+};
+
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((address_space(3))) s16x4_t* ls16x4p;
 
@@ -517,13 +528,14 @@ __global__ void __launch_bounds__(256 * GROUPS, 2) attn_prompt_kernel(AttnArgs a
         *(u32x4_t*)(a.out + ((int64_t)(rt.first + q_at) * a.Hq + (int64_t)head * G + in_group) * D + 8 * col) = y;
     }
   } else if (wave * 32 + r < rows) {
-    const int64_t at = ((int64_t)unit * plan.splits + split) * kTileRows + wave * 32 + r;
+    const Parts parts{(int64_t)a.T * G, Hkv, plan.splits};
+    const int64_t at = parts.at(head, split, (int64_t)rt.first * G + rt.row0 + wave * 32 + r);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int e = 0; e < 16; e += 4)
         *(at_f32x4*)(a.ws + at * D + 32 * dt + 2 * e + 4 * j) = at_f32x4{o[dt][e], o[dt][e + 1], o[dt][e + 2], o[dt][e + 3]};
-    if (j == 0) *(float2*)(a.ws + plan.tiles * Hkv * plan.splits * kTileRows * D + at * 2) = make_float2(m, sum);
+    if (j == 0) *(float2*)(a.ws + parts.stats(D) + at * 2) = make_float2(m, sum);
   }
 }
 
@@ -537,8 +549,9 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(AttnArgs a, Promp
   const Keys keys(rt, plan);
   const int parts = keys.parts(), l = threadIdx.x % LANES, row = blockIdx.y * ROWS + threadIdx.x / LANES;
   if (parts == 1 || row >= rt.n * G - rt.row0) return;
-  const float* __restrict__ stats = a.ws + plan.tiles * Hkv * plan.splits * kTileRows * D;
-  auto slot = [&](int s) { return ((int64_t)unit * plan.splits + s) * kTileRows + row; };
+  const Parts held{(int64_t)a.T * G, Hkv, plan.splits};
+  const float* __restrict__ stats = a.ws + held.stats(D);
+  auto slot = [&](int s) { return held.at(head, s, (int64_t)rt.first * G + rt.row0 + row); };
   // lane l of a row's has the maxima and sums of parts l, LANES + l, ..., then every lane those of all
   float most = kNegInf, total = 0.0f, mine_m[kMaxSplits / LANES], mine_w[kMaxSplits / LANES];
 #pragma unroll
@@ -590,7 +603,7 @@ void launch(const AttnArgs& a, const PromptPlan& p, hipStream_t stream) {
 
 size_t attn_prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys) {
   const PromptPlan p = plan_of(T, B, Hq, Hkv, keys);
-  return p.splits > 1 ? (size_t)(p.tiles * Hkv * p.splits * kTileRows * (D + 2)) * sizeof(float) : 0;
+  return p.splits > 1 ? (size_t)Parts{T * p.G, (int)Hkv, p.splits}.size((int)D) * sizeof(float) : 0;
 }
 int64_t attn_prompt_blocks(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t, int64_t keys) {
   const PromptPlan p = plan_of(T, B, Hq, Hkv, keys);

@@ -545,7 +545,7 @@ ql_status qlinear_attn_decode(const ql_kv_cache *cache, int64_t B, int64_t Hq, c
  * holds already: query i sees tokens 0 .. lens[b] - n + i (none: 0 comes out, where lens[b] < n).  Rows that
  * belong to no sequence are not written.  All else as for qlinear_attn_decode.
  *   q, out (dev) bf16 bits [T][Hq][dim]; starts (dev) int32 [B + 1], ascending, cut to 0 .. T; T * Hq is below
- *   2^31; workspace of qlinear_attn_prompt_workspace_bytes, where few rows meet many keys, else 0. */
+ *   2^31; workspace of qlinear_attn_prompt_workspace_bytes, where few rows meet many keys (34 MB at most), else 0. */
 size_t qlinear_attn_prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys);
 ql_status qlinear_attn_prompt(const ql_kv_cache *cache, int64_t T, int64_t B, int64_t Hq, const uint16_t *q,
                               const int32_t *starts, const int32_t *table, int64_t table_stride, int64_t max_pages,

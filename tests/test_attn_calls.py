@@ -130,3 +130,14 @@ def test_a_cache_follows_its_tensors_shape(launches):
     ql.attn_decode(zeros(1, 4, 128), c, ints(1, 3), ints(1))
     d = passed(launches[-1][1], ql.ql_kv_cache)
     assert (d.pages, d.heads, d.page, d.dim) == (5, 1, 32, 128)
+
+
+@pytest.mark.parametrize("T,B,Hq,Hkv,D,keys", [(64, 64, 32, 8, 128, 8192), (256, 64, 32, 8, 128, 8192), (256, 256, 32, 8, 128, 8192),
+                                               (70, 70, 32, 8, 128, 131072), (2048, 2048, 8, 8, 128, 8192), (16384, 16384, 1, 1, 128, 8192),
+                                               (1, 1, 32, 8, 128, 131072), (9, 1, 128, 1, 64, 1 << 20), (300, 7, 40, 8, 128, 32768),
+                                               (5, 3000, 32, 8, 128, 4096), (1025, 1025, 14, 2, 64, 65536)])
+def test_a_prompts_workspace_is_for_its_rows(T, B, Hq, Hkv, D, keys):
+    """Parts hold the rows that there are, not a tile of 128 for each sequence (1072 MiB for 64 sequences of one): the rows
+    that are split fill at most 512 tiles of 128, each of D sums and two numbers."""
+    need = ql.lib().qlinear_attn_prompt_workspace_bytes(T, B, Hq, Hkv, D, keys)
+    assert 0 < need <= 512 * 128 * (D + 2) * 4 and need % (T * Hq * (D + 2) * 4) == 0
