@@ -52,12 +52,14 @@ typedef __attribute__((ext_vector_type(4))) float at_f32x4;
 typedef __attribute__((ext_vector_type(16))) float at_f32x16;
 
 constexpr float kNegInf = -__builtin_inff();
-// Weights are exp2(score - maximum - kRoom): up to 2^8 by the maximum in use, so that 2^30 of them times the largest values
-// stay in fp32's range (2^30 2^128 2^8 2^-39 = 2^127).  The factor cancels out; a weight's exponent is rounded in
-// steps of 2^-18, 2^-19 off, where a bf16 weight is off by 2^-9.
-constexpr float kRoom = 39.0f;
-
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Weights are exp2(score - maximum - room), the maximum in use being `lag` below a score at most, so that those of a
+// sequence's len tokens sum to 1/2 at most and times the largest values stay in fp32's range.  The room is no larger than
+// that, as at the other end of the range values lose what it takes (with room for 2^30 tokens, V of 2^-112 came out
+// as 0 for one).  It is one for all parts of a row, so it cancels out; up to 39 as it is, it puts a weight's exponent off by
+// 2^-19, where a bf16 weight is off by 2^-8.
+__device__ __forceinline__ float room_of(int len, float lag) { return lag + (float)(33 - __builtin_clz(len | 1)); }
 
 // what a call reads once: not kept in the caches
 template <class P>

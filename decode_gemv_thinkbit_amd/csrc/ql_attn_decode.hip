@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
     }
   }
   const float c = a.score_scale * (a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
+  const float room = room_of(at.len, 0.0f);
 
   const int32_t* __restrict__ row = a.table + at.b * a.table_stride;
   const int shift = a.kv.page_shift;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
     const float m_new = fmaxf(m, top);
     const float alpha = part_weight(m, m_new);
     m = m_new;
-    const float base = m == kNegInf ? 0.0f : m + kRoom;
+    const float base = m == kNegInf ? 0.0f : m + room;
     sum *= alpha;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) attn_decode_kernel(AttnArgs a,
       p[i] = exp2_fast(p[i] - base);
       sum += p[i];
     }
-    // exp2 rounded to bf16, half a step of 2^-9 each; the sum is of the unrounded ones
+    // exp2 rounded to bf16, half a step of 2^-8 each; the sum is of the unrounded ones
     const u32x4_t pw{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])};
     const at_bf16x8 pv = __builtin_bit_cast(at_bf16x8, pw);
 #pragma unroll

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(256 * GROUPS, 2) attn_prompt_kernel(AttnArgs a
     for (int i = 0; i < DK; ++i) qf[i] = *(gu32x4p)(p + 16 * i);
   }
   const float c = a.score_scale * (a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
+  const float room = room_of(rt.len, kLag);
 
   struct Source { const uint8_t *k, *v; int bad; };
   auto source = [&](int t, int e) {
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(256 * GROUPS, 2) attn_prompt_kernel(AttnArgs a
       for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
       top = max_xor32(top) * c;
       // The maximum in use follows only when some row's scores pass it by 2^kLag (the result is the same: it
-      // cancels out, and kRoom has place for weights of 2^8)
+      // cancels out, and the room has place for weights of 2^kLag)
       if (__ballot(top > m + kLag)) {
         const float m_new = fmaxf(m, top), alpha = part_weight(m, m_new);
         m = m_new;
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(256 * GROUPS, 2) attn_prompt_kernel(AttnArgs a
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
       }
-      const float base = m == kNegInf ? 0.0f : m + kRoom;
+      const float base = m == kNegInf ? 0.0f : m + room;
       u32x4_t pf[4];
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {

@@ -529,7 +529,8 @@ ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void *q, i
  * sequence's pages in order.  A sequence of no tokens gives 0; lengths are cut to what a row of the table
  * holds; entries that are no page of the cache stand for tokens that are not seen.  What memory behind a
  * sequence's last token holds does not matter.  Softmax statistics and sums are fp32, its weights bf16 as
- * they enter the second product.  Deterministic for given B, lens and heads.
+ * they enter the second product.  fp32's steps end at 2^-149: a result of n tokens may be off by n (n + 40) 2^-148 (a
+ * prompt's by 2^8 times that), which values of less than 2^-100 can feel.  Deterministic for given B, lens and heads.
  *   q (dev) bf16 bits [B][Hq][dim]; table (dev) int32 [B][max_pages], row b at b * table_stride; lens (dev)
  *   int32 [B]; scale > 0; out (dev) bf16 bits [B][Hq][dim]; workspace (dev, 16-byte aligned, contents need not
  *   be zeroed) of qlinear_attn_decode_workspace_bytes, the parts of long sequences; 0 (then NULL will do) if

@@ -72,3 +72,65 @@ def test_parts_of_prompts_stay_in_their_workspace(dev, new, before, front, behin
     assert ref.bf16_close(out.cpu()[rows], want[rows], slack[rows]).all()
     assert (out[:front] == 5.0).all() and (out[starts[-1] :] == 5.0).all()
     assert torch.isnan(buf[:1024]).all() and torch.isnan(buf[-1024:]).all()
+
+
+# ---------------------------------------------------------------- the ends of bf16's range
+def of_size(seqs, exponent):
+    """V positive, and 2^exponent times as large."""
+    seqs.v = (seqs.v.float().abs() * 2.0 ** exponent).to(torch.bfloat16)
+    for both in seqs.kv:
+        both[1] = both[1].abs() * 2.0 ** exponent
+    return seqs
+
+
+def steps_below(n, lag):
+    """What fp32's last step moves a result: n products and some 40 sums of parts are off by 2^-150 each, and the largest
+    weight is 2^-room at least, with 2^room at most 4 n 2^lag."""
+    return (n + 40) * 2.0 ** -150 * 4 * n * 2.0 ** lag
+
+
+@pytest.mark.parametrize("lens", [[1], [2, 17, 500], [700, 3, 40], [9000]])
+def test_decode_small_values(dev, lens):
+    """V far below 1, where bf16 is still normal: nothing of it is lost among fp32's last steps but what they are."""
+    seqs = of_size(ref.Sequences(lens, 2, 64, 16, seed=5), -112)
+    q = ref.queries(len(lens), 4, 64, 6)
+    want, slack = ref.decode(seqs, q, 64 ** -0.5)
+    slack = slack + torch.tensor([steps_below(n, 0) for n in lens])[:, None, None]
+    got = ql.attn_decode(q.to(dev), *seqs.on(dev)).cpu()
+    assert ref.bf16_close(got, want, slack).all()
+
+
+@pytest.mark.parametrize("n,length", [(1, 1), (20, 20), (300, 300), (700, 700), (5, 4000), (300, 4000)])
+def test_prompt_small_values(dev, n, length):
+    seqs = of_size(ref.Sequences([length], 2, 128, 16, seed=5), -112)
+    q = ref.queries(n, 4, 128, 6)
+    cache, table, lens = seqs.on(dev)
+    got = ql.attn_prompt(q.to(dev), ints([0, n], dev), cache, table, lens).cpu()
+    want, slack = ref.prompt(seqs, q, [0, n], 128 ** -0.5)
+    assert ref.bf16_close(got, want, slack + steps_below(length, 8)).all()
+
+
+@pytest.mark.parametrize("length", [1, 64, 127, 512, 513, 4095, 20000])
+@pytest.mark.parametrize("exponent", [127, -118])
+@pytest.mark.parametrize("lag", [0.0, 7.9])
+def test_the_largest_sums_of_weights(dev, length, exponent, lag):
+    """All of V one value, all keys but the first 64 weighing 2^lag times as much as those, which a maximum that follows
+    only larger steps leaves as they are: the value comes out."""
+    D, page = 64, 64
+    pages = (length + page - 1) // page
+    k = torch.zeros(pages, 1, page, D)
+    k[1:, :, :, 0] = lag  # one score of q . k = lag, exact in the scale below
+    k = k.to(torch.bfloat16)
+    v = torch.full((pages, 1, page, D), 2.0 ** exponent).to(torch.bfloat16)
+    cache = ql.KvCache(k.to(dev), v.to(dev))
+    q = torch.zeros(3, 2, D, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    q = q.to(dev)
+    table = torch.arange(pages, dtype=torch.int32, device=dev).view(1, -1)
+    scale = 0.6931471805599453  # of q . k in powers of two
+    # the weights' bf16 rounding, the output's, and the sums' (exponents of weights are off by 2^-18 at most)
+    near = lambda got: ((got.cpu().double() / 2.0 ** exponent - 1).abs() <=
+                        2 * ref.EPS16 + 2 * (length + 40) * ref.EPS32 + steps_below(length, 8) / 2.0 ** exponent + 2.0 ** -18).all()
+    assert near(ql.attn_decode(q[:1], cache, table, ints([length], dev), scale=scale))
+    n = min(3, length)
+    assert near(ql.attn_prompt(q[:n], ints([0, n], dev), cache, table, ints([length], dev), scale=scale))
