@@ -633,7 +633,7 @@ static ql_status check_cache(const ql_kv_cache* c, int64_t Hq, ql::KvArgs* kv) {
 
 static ql_status check_rows(int64_t T, int64_t heads, int64_t dim, int dtype, const void* p, int64_t stride) {
   QL_TRY(check_ptrs({p}));
-  if (stride % (dtype == QL_F32 ? 4 : 8) || (T > 1 && stride < heads * dim) || stride < 0 || stride > (int64_t)1 << 32)
+  if (T > 1 && (stride % (dtype == QL_F32 ? 4 : 8) || stride < heads * dim || stride > (int64_t)1 << 32))
     return fail(QL_EINVAL, "rows of %lld values need a stride of at least as many, a multiple of 16 bytes (stride=%lld)",
                 (long long)(heads * dim), (long long)stride);
   return QL_OK;

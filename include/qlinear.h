@@ -514,10 +514,11 @@ typedef struct {
 } ql_rope;
 
 /* q [T][Hq][dim], k and v [T][heads][dim] of type dtype (QL_F32, QL_BF16, QL_F16), token t at t * stride
- * elements (a multiple of 16 bytes, so they may be parts of one wider row): q and k are normed if q_norm /
- * k_norm are not NULL (x * norm / sqrt(mean of the head's x^2 + eps), norm (dev) fp32 [dim]) and turned; q is
- * written to out (dev) bf16 bits [T][Hq][dim], k and v to slot slots[t] of the cache (e4m3: x / scale, what is
- * over 448 as 448).  A slot that is not in the cache (-1: a padded token) is left out; no slot may appear twice.
+ * elements (a multiple of 16 bytes, so they may be parts of one wider row; any value where T is 1): q and k are
+ * normed if q_norm / k_norm are not NULL (x * norm / sqrt(mean of the head's x^2 + eps), norm (dev) fp32 [dim])
+ * and turned; q is written to out (dev) bf16 bits [T][Hq][dim], k and v to slot slots[t] of the cache (e4m3:
+ * x / scale, what is over 448 as 448).  A slot that is not in the cache (-1: a padded token) is left out; no slot
+ * may appear twice.
  *   positions, slots (dev) int32 [T]; 1 <= T < 2^24. */
 ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void *q, int64_t q_stride, const void *k,
                               int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,

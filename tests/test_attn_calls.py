@@ -141,3 +141,11 @@ def test_a_prompts_workspace_is_for_its_rows(T, B, Hq, Hkv, D, keys):
     that are split fill at most 512 tiles of 128, each of D sums and two numbers."""
     need = ql.lib().qlinear_attn_prompt_workspace_bytes(T, B, Hq, Hkv, D, keys)
     assert 0 < need <= 512 * 128 * (D + 2) * 4 and need % (T * Hq * (D + 2) * 4) == 0
+
+
+@pytest.mark.parametrize("strides", [dict(qs=1), dict(ks=1, vs=3), dict(qs=0, ks=0, vs=0), dict(dtype=1, qs=1 << 40)])
+def test_a_single_row_has_no_stride(strides):
+    """No distance is taken from it: a tensor of one row may have any (torch.empty(N, 1).t() is contiguous)."""
+    import test_attn as calls
+
+    assert calls.rope_call(T=1, out=calls.ODD, **strides) == 1 and "aligned" in calls.message(), calls.message()

@@ -134,3 +134,20 @@ def test_the_largest_sums_of_weights(dev, length, exponent, lag):
     assert near(ql.attn_decode(q[:1], cache, table, ints([length], dev), scale=scale))
     n = min(3, length)
     assert near(ql.attn_prompt(q[:n], ints([0, n], dev), cache, table, ints([length], dev), scale=scale))
+
+
+@pytest.mark.parametrize("ty", [torch.float32, torch.bfloat16])
+def test_one_token_of_any_stride(dev, ty):
+    Hq, Hkv, D = 4, 2, 64
+    rows = [torch.randn(1, h * D, generator=torch.Generator().manual_seed(h)).to(ty).to(dev) for h in (Hq, Hkv, Hkv)]
+    odd = [torch.empty(x.shape[1], 1, dtype=ty, device=dev).t().copy_(x) for x in rows]
+    assert all(x.is_contiguous() and x.stride() == (1, 1) for x in odd)
+    rope = ql.Rope(torch.rand(D // 2, device=dev))
+    results = []
+    for q, k, v in (rows, odd):
+        cache = ql.KvCache(*(torch.zeros(1, Hkv, 16, D, dtype=torch.bfloat16, device=dev) for _ in "kv"))
+        turned = ql.rope_append(q, k, v, ints([7], dev), ints([3], dev), rope, cache)
+        y = ql.attn_decode(turned, cache, ints([[0]], dev), ints([4], dev))
+        z = ql.attn_prompt(turned.t().contiguous().t(), ints([0, 1], dev), cache, ints([[0]], dev), ints([4], dev))
+        results.append((turned, cache.k, cache.v, y, z))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
