@@ -68,14 +68,28 @@ __global__ void __launch_bounds__(256) rope_append_kernel(RopeArgs a) {
   }
   const float* norm = is_q ? a.q_norm : a.k_norm;
   if (norm && (is_q || is_k)) {
-    float sum = 0.0f;
+    float by[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
+    for (int i = 0; i < 8; ++i) by[i] = norm[part * 8 + i];
+    auto squares = [&] {
+      float sum = 0.0f;
 #pragma unroll
-    for (int m = 1; m < LANES; m *= 2) sum += __shfl_xor(sum, m);
-    const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+      for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * norm[part * 8 + i];
+      for (int m = 1; m < LANES; m *= 2) sum += __shfl_xor(sum, m);
+      return sum;
+    };
+    const float mean = squares() * (1.0f / D) + a.eps;
+    float r = 1.0f / sqrtf(mean);
+    if (__builtin_expect(!(mean < 0x1p119f && mean > 0x1p-100f), 0)) {
+      // fp32 may not hold the squares: those of x times a power of two, which cancels out
+      const float f = mean < 1.0f ? 0x1p100f : 0x1p-70f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= f;
+      r = 1.0f / sqrtf(squares() * (1.0f / D) + a.eps * f * f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * by[i];
   }
   {
     at_f32x4* at = (at_f32x4*)&xs[slot_in][part * 8];

@@ -151,3 +151,26 @@ def test_one_token_of_any_stride(dev, ty):
         z = ql.attn_prompt(turned.t().contiguous().t(), ints([0, 1], dev), cache, ints([[0]], dev), ints([4], dev))
         results.append((turned, cache.k, cache.v, y, z))
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("ty", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("spread,eps", [(1e30, 1e-6), (1e37, 0.0), (1e19, 1e-6), (1e18, 1e38), (1e-12, 0.0), (1e-18, 1e-36), (1e-22, 0.0),
+                                        (1e-30, 1e-38), (1e-36, 0.0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_norms_of_any_size(dev, ty, spread, eps, D):
+    """Squares that fp32 does not hold: the norm is what it is for any other size."""
+    T, H = 5, 3
+    g = torch.Generator().manual_seed(D)
+    x = (torch.randn(T, H, D, generator=g) * spread).to(ty)
+    x[:, 1] *= 2.0 ** -10  # heads of another size beside
+    norm = 1 + 0.2 * torch.randn(D, generator=g)
+    positions = torch.arange(T, dtype=torch.int32)
+    freqs = torch.rand(D // 2, generator=g)
+    cache = ql.KvCache(*(torch.zeros(1, H, 16, D, dtype=torch.bfloat16, device=dev) for _ in "kv"))
+    got = ql.rope_append(*(x.to(dev),) * 3, positions.to(dev), positions.to(dev), ql.Rope(freqs.to(dev)), cache, q_norm=norm.to(dev),
+                         k_norm=norm.to(dev), eps=eps)
+    want, slack = ref.turned(x, positions, freqs, False, 1.0, norm, torch.tensor(eps, dtype=torch.float32).double())
+    # (an eps of fewer bits, fp32's last step beside it)
+    slack = slack + (2.0 ** -150 / eps if eps else 0.0) * want.abs()
+    assert ref.bf16_close(got.cpu(), want, slack).all()
+    assert ref.bf16_close(cache.k.cpu()[0, :, :T].transpose(0, 1), want, slack).all()
