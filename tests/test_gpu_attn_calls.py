@@ -174,3 +174,32 @@ def test_norms_of_any_size(dev, ty, spread, eps, D):
     slack = slack + (2.0 ** -150 / eps if eps else 0.0) * want.abs()
     assert ref.bf16_close(got.cpu(), want, slack).all()
     assert ref.bf16_close(cache.k.cpu()[0, :, :T].transpose(0, 1), want, slack).all()
+
+
+@pytest.mark.parametrize("starts,ranges", [([-3, 20, 10, 10], [(0, 20), (20, 20), (10, 10)]), ([0, 25, 10 ** 9], [(0, 25), (25, 40)]),
+                                           ([-(2 ** 31), -1, 7, 2 ** 31 - 1], [(0, 0), (0, 7), (7, 40)]), ([50, 60, 10 ** 9], [(40, 40)] * 2)])
+@pytest.mark.parametrize("length", [40, 3000])
+def test_rows_of_cut_starts(dev, starts, ranges, length):
+    """starts are cut to 0 .. T, a range that ends before it begins is empty; the rows left have their results, no other row
+    is written, and none around q is read into them."""
+    T, Hq, D = 40, 2, 64
+    seqs = ref.Sequences([length] * len(ranges), 1, D, 16, seed=8)
+    cache, table, lens = seqs.on(dev)
+    room = 200 * Hq * D
+    held = torch.full((T * Hq * D + 2 * room,), float("nan"), dtype=torch.bfloat16, device=dev)
+    out = torch.full_like(held, 5.0)
+    q, y = (t[room:-room].view(T, Hq, D) for t in (held, out))
+    q.copy_(ref.queries(T, Hq, D, 9))
+    ql.attn_prompt(q, ints(starts, dev), cache, table, lens, out=y)
+    assert (out[:room] == 5.0).all() and (out[-room:] == 5.0).all()
+    mine = torch.zeros(T, dtype=torch.bool)
+    y, host = y.cpu(), q.cpu()
+    for b, (first, end) in enumerate(ranges):
+        if first == end:
+            continue
+        mine[first:end] = True
+        k, v = seqs.kv[b]
+        sees = torch.arange(length)[None] <= length - (end - first) + torch.arange(end - first)[:, None]
+        want, slack = ref.attention(host[first:end], k, v, sees, D ** -0.5)
+        assert ref.bf16_close(y[first:end], want, slack).all()
+    assert (y[~mine] == 5.0).all()
