@@ -22,3 +22,9 @@ def test_wait_states_before_loads(kernels, src):
 @pytest.mark.parametrize("src", SOURCES)
 def test_loads_end_before_the_kernel(kernels, src):
     rules.test_loads_end_before_the_kernel(kernels, src)
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_all_lanes_return(kernels, src):
+    assert any(op == "s_mov_b32" and operands[0] == "exec_hi" for code in kernels[src].values() for op, operands in code)
+    rules.test_all_lanes_return(kernels, src)
