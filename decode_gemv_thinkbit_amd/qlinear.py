@@ -881,7 +881,10 @@ def rope_frequencies(dims: int, base: float = 10000.0, stretch: float = 1.0, ori
     `stretch` times as long divided by stretch (positions squeezed linearly) or, with the `original` context
     length, by parts: pairs that turn more than `fast` times within it keep their frequency, those that turn
     less than `slow` times are divided by stretch, the ones between are mixed by a ramp over the pairs' number,
-    and factor is 0.1 ln(stretch) + 1."""
+    and factor is 0.1 ln(stretch) + 1.  The parts, their bounds' rounding and the factor are as published with the YaRN
+    method (Peng, Quesnelle, Fan, Shippole: "YaRN: Efficient Context Window Extension of Large Language Models",
+    2023), by which models were trained; linear squeezing is Chen et al., "Extending Context Window of Large
+    Language Models via Positional Interpolation", 2023."""
     if dims < 2 or dims % 2 or not base > 1 or not stretch >= 1 or not fast > slow > 0 or \
             (original is not None and original < 1):
         raise ValueError("an even number of dims, base > 1, stretch >= 1, fast > slow > 0, original >= 1")

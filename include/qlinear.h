@@ -494,7 +494,7 @@ ql_status qlinear_mx4_moe(const ql_mx4_experts *experts, int64_t T, const uint16
  * Slot number i is place i % page of page i / page.  dim is 64 or 128; page a power of two, 16 .. 4096;
  * pages * page is below 2^31.  Arrays of int32 and small fp32 ones (scales, norms, freqs) need an alignment
  * of 4 bytes only.  Values that are not finite are taken as they are: a row that sees them is not finite, the others
- * are as without them. */
+ * are as without them.  (A key whose score is minus infinity weighs 0; if all of a row's do, it is 0.) */
 typedef struct {
   int32_t pages, heads, page, dim;
   int32_t type; /* ql_dtype: QL_BF16 or QL_E4M3 */
@@ -531,12 +531,15 @@ ql_status qlinear_rope_append(int64_t T, int64_t Hq, int dtype, const void *q, i
  * holds; entries that are no page of the cache stand for tokens that are not seen.  What memory behind a
  * sequence's last token holds does not matter.  Softmax statistics and sums are fp32, its weights bf16 as
  * they enter the second product.  fp32's steps end at 2^-149: a result of n tokens may be off by n (n + 40) 2^-148 (a
- * prompt's by 2^8 times that), which values of less than 2^-100 can feel.  Deterministic for given B, lens and heads.
+ * prompt's by 2^8 times that), which values of less than 2^-100 can feel.  The same bits for the same B, Hq, heads,
+ * max_pages * page and lens (for prompts T and starts too); behind a table of another width the same sequences may be
+ * summed in other parts.
  *   q (dev) bf16 bits [B][Hq][dim]; table (dev) int32 [B][max_pages], row b at b * table_stride; lens (dev)
  *   int32 [B]; scale > 0; out (dev) bf16 bits [B][Hq][dim]; workspace (dev, 16-byte aligned, contents need not
  *   be zeroed) of qlinear_attn_decode_workspace_bytes, the parts of long sequences; 0 (then NULL will do) if
  *   rows of the table are short.  Calls that share a workspace must not overlap.
- * Hq is a multiple of heads; max_pages * page (keys, in the size) is at most 2^30. */
+ * Hq is a multiple of heads; max_pages * page (keys, in the size) is at most 2^30.  Work is shared out on the device,
+ * where every workgroup reads all lengths: more than some thousands of sequences are better served by several calls. */
 size_t qlinear_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim, int64_t keys);
 ql_status qlinear_attn_decode(const ql_kv_cache *cache, int64_t B, int64_t Hq, const uint16_t *q,
                               const int32_t *table, int64_t table_stride, int64_t max_pages, const int32_t *lens,

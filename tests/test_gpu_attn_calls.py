@@ -203,3 +203,19 @@ def test_rows_of_cut_starts(dev, starts, ranges, length):
         want, slack = ref.attention(host[first:end], k, v, sees, D ** -0.5)
         assert ref.bf16_close(y[first:end], want, slack).all()
     assert (y[~mine] == 5.0).all()
+
+
+def test_scores_of_minus_infinity(dev):
+    """Such a key weighs 0, and a row of no other keys is 0."""
+    D, n = 64, 40
+    seqs = ref.Sequences([n, 5], 1, D, 16, seed=2)
+    q = ref.queries(2, 2, D, 3).abs() + 1
+    visible = torch.ones(n, dtype=torch.bool)
+    for i in (3, 17, 39):
+        seqs.k[seqs.table[0, i // 16], 0, i % 16, 5] = -float("inf")
+        visible[i] = False
+    seqs.k[seqs.table[1, 0], 0, :5, 7] = -float("inf")
+    cache, table, lens = seqs.on(dev)
+    want, slack = ref.decode(seqs, q, D ** -0.5, {0: visible})
+    for got in (ql.attn_decode(q.to(dev), cache, table, lens), ql.attn_prompt(q.to(dev), ints([0, 1, 2], dev), cache, table, lens)):
+        assert ref.bf16_close(got.cpu()[:1], want[:1], slack[:1]).all() and (got[1] == 0).all()
