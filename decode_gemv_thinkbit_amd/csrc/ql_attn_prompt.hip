@@ -45,10 +45,12 @@ struct PromptPlan {
   int groups;            // of four waves
   int64_t tiles;         // row tiles of a kv head at most
 };
-// Two workgroups fit a CU: where the rows do not make that many, the keys are split.  A part costs its rows' sums
-// in fp32 written and read, so parts are long but where rows are few (32 over 8 heads of 128: 512 tokens take 16.8 us
-// in one part, 20.7 in two of 256 keys; 64 tokens behind 4000 29.6 us in parts of 128 keys, 24.0 of 256,
-// 24.9 of 512; 4 behind 1000 17.1 in parts of 512, 13.0 of 256).
+// Two workgroups fit a CU (of heads of 64 in bf16 three, which the plan does not use): where the rows do not make that
+// many, the keys are split.  A part costs its rows' sums in fp32 written and read, so parts are long but where rows are
+// few (32 over 8 heads of 128: 512 tokens take 15.5 us in one part, 22.3 in two of 256 keys; 64 tokens behind 4000
+// 29.3 us in parts of 128 keys, 23.0 of 256, 24.0 of 512; 4 behind 1000 16.6 in parts of 512, 13.0 of 256).
+// `keys` is what a row of the table holds, not a length: behind a table much wider than the prompt most parts are empty
+// (200 tokens 10.2 us, 15.0 with a table of 8192; 1024 tokens 23.9 and 33.3).
 PromptPlan plan_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t keys) {
   PromptPlan p;
   p.G = (int)(Hq / Hkv);
@@ -56,11 +58,20 @@ PromptPlan plan_of(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t keys) 
   p.least = T * p.G <= 2 * kTileRows ? 4 : 16;
   const int64_t blocks = (T * p.G + kTileRows - 1) / kTileRows * Hkv;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / blocks, keys / (p.least * kTileKeys), kMaxSplits}));
-  // Where a CU gets one workgroup or little more, two groups of waves take turns at a row tile's keys: 1024 tokens, 32 over
-  // 8 heads of 128, 26.4 us, then 23.5; 512 15.8 and 15.2; 200 behind 3000 33.9 and 30.2; with two workgroups for a CU,
-  // 1500 tokens 37.0 and 33.4, 2048 49.5 and 47.1, with more no longer (3000 84.0 and 94.8).  Joining them takes 2 us, too
-  // much for short rows (200 tokens 10.1 and 11.1; four sequences of 125 .. 875 26.3 and 30.5) and for the short parts of
-  // few rows (16 behind 16000 29.0 and 30.0).
+  // Where a CU gets one workgroup or little more, two groups of waves take turns at a row tile's keys.  Microseconds with
+  // one group and two, 32 over 8 heads:
+  //              of 128, bf16   e4m3          of 64, bf16   e4m3
+  //   200 tokens  10.1   11.1   10.8   11.5    8.0    8.2    8.4    8.5
+  //   300         12.1   12.7   12.9   13.6    9.4    9.6    9.9    9.9
+  //   512         15.9   15.1   17.1   16.4   12.1   11.3   12.9   11.9
+  //   1024        26.7   23.4   28.4   25.7   19.6   16.9   21.0   18.1
+  //   1500        36.6   32.9   39.4   34.5   26.7   21.9   28.7   24.1
+  //   2048        49.3   48.0   51.1   51.3   34.7   32.7   37.0   36.1
+  //   3000        83.3   95.3   86.2  102.7   54.9   64.7   57.6   73.2
+  //   200 behind 3000
+  //               34.5   30.6   36.8   34.1   25.7   23.0   27.0   23.8
+  // Joining them takes 2 us, too much for short rows and for the short parts of few rows (16 behind 16000, of 128 in bf16,
+  // 29.0 and 30.0).
   const int64_t units = (T * p.G + (B - 1) * (kTileRows / 2) + kTileRows - 1) / kTileRows * Hkv * p.splits;  // about
   const bool two = p.splits > 1    ? units <= 256 && T * p.G > 2 * kTileRows
                    : units <= 256 ? T >= 300 * B
@@ -80,8 +91,8 @@ __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(
 // batch's order; 13 packed sequences of 47 .. 1189 tokens 89 and 93; 60 of 1 .. 158 21.2 either way.  The longest tiles
 // of all sequences first were slower: workgroups that run together then share no keys.)
 // Tiles `layer` .. 2 layer - 1, the second workgroups of the CUs (of one group of waves), are taken from their end, so
-// that the longest of the first and the shortest of the second share a CU (4096 tokens, 32 over 8 heads of 128: 148 us,
-// 152 without).
+// that the longest of the first and the shortest of the second share a CU (4096 tokens, 32 over 8 heads of 128: 143 us,
+// 148 without, in e4m3 147 and 155; of 64 86.8 and 87.3, in e4m3 96.6 and 103).
 __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int G, int want, int layer) {
   const int lane = threadIdx.x & 63;
   uint32_t before = 0;

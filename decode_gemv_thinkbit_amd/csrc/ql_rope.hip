@@ -43,7 +43,9 @@ __device__ __forceinline__ u32x4_t bf16x8(const float (&x)[8]) {
 // pair's other half is in another lane: heads meet in LDS.
 //
 // Memory bounds: 8192 tokens of 40 + 2 x 8 heads of 128 (346 MB, fp32 in, bf16 out) take 67 us, 5.1 TB/s, where a
-// large copy reaches 4.9.  One token is a launch and two memory latencies, 3.8 us.
+// large copy reaches 4.9.  bf16 or fp16 in (231 MB) takes 61, 3.8 TB/s, without norms 54: there the waves' own time counts
+// too (norms' sums over lanes, sines, the pairs' way through LDS).  e4m3 pages, a division a value, cost 2 to 3 us
+// more for 16 MB less.  One token is a launch and two memory latencies, 3.8 us.
 template <int TYPE, int D, bool F8>
 __global__ void __launch_bounds__(256) rope_append_kernel(RopeArgs a) {
   constexpr int LANES = D / 8, HEADS = 256 / LANES;
