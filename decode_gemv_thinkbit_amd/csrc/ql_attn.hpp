@@ -57,7 +57,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // Weights are exp2(score - maximum - room), the maximum in use being `lag` below a score at most, so that those of a
 // sequence's len tokens sum to 1/2 at most and times the largest values stay in fp32's range.  The room is no larger than
 // that, as at the other end of the range values lose what it takes (with room for 2^30 tokens, V of 2^-112 came out
-// as 0 for one).  It is one for all parts of a row, so it cancels out; up to 39 as it is, it puts a weight's exponent off by
+// as 0 for one).  It is one for all parts of a row, so it cancels out; up to 40 as it is, it puts a weight's exponent off by
 // 2^-19, where a bf16 weight is off by 2^-8.
 __device__ __forceinline__ float room_of(int len, float lag) { return lag + (float)(33 - __builtin_clz(len | 1)); }
 
